@@ -332,6 +332,60 @@ moe_status_t moe_layer_backward(const moe_layer_desc_t* desc, const moe_bf16_t* 
 moe_status_t moe_update_router_bias(const int32_t* counts, int E, float gamma, float* bias,
                                     moe_stream_t stream);
 
+/* ----------------------------------------------------------------------------------------
+ * Products grouped by expert over ragged rows: the plain linear layer of an expert and its two
+ * gradients, for experts that are not the SwiGLU of moe_grouped_swiglu_ffn, or whose sizes or types
+ * it does not take.  Rows of segment e are [offsets[e], offsets[e+1]) (moe_permute's offsets):
+ *   moe_grouped_gemm        y[r]  = x[r] W_e^T      x  [M, K], w [E, N, K] -> y  [M, N]
+ *   moe_grouped_gemm_dgrad  dx[r] = dy[r] W_e       dy [M, N], w [E, N, K] -> dx [M, K]
+ *   moe_grouped_gemm_wgrad  dw[e] = dy_e^T x_e      dy [M, N], x [M, K]    -> dw [E, N, K] fp32
+ *   dtype      MOE_DTYPE_BF16 or MOE_DTYPE_FP16: the type of every 16-bit tensor of the call
+ *   out_dtype  of y / dx: dtype, or MOE_DTYPE_FP32
+ *   offsets    [E+1] int32 (device).  Rows of y / dx outside every segment are not written; an expert
+ *              without rows gets dw[e] = 0.  Offsets that decrease or leave [0, M] set
+ *              MOE_ERR_DEVICE_INDEX in the error word and are clamped (the results of the segments
+ *              they bound are then unspecified).
+ * Sums are accumulated in fp32 and rounded once; a sum of a long segment into fp32 is as exact as
+ * fp32 additions in a fixed order.  Results do not depend on timing.  dw is overwritten.
+ * N and K are multiples of 8 up to 65536; 1 <= E <= 1024; M >= 0 (M = 0: y / dx empty, dw zeros).
+ * Any number of rows per segment; few rows (one token) stream the active experts' weights once.
+ *   ws: at least the matching _workspace_size() bytes, zero-filled before its first use (later calls of
+ *       these entry points and of moe_orthogonalize may share it, one at a time; zero it again after a
+ *       MOE_ERR_TIMEOUT); first 256 bytes: the device error word.
+ * ---------------------------------------------------------------------------------------- */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_FP16 1
+#define MOE_DTYPE_FP32 2
+
+size_t moe_grouped_gemm_workspace_size(int M); /* moe_grouped_gemm and moe_grouped_gemm_dgrad */
+moe_status_t moe_grouped_gemm(const void* x, const int32_t* offsets, const void* w, int M, int E, int N, int K,
+                              int dtype, int out_dtype, void* y, void* ws, size_t ws_bytes, moe_stream_t stream);
+moe_status_t moe_grouped_gemm_dgrad(const void* dy, const int32_t* offsets, const void* w, int M, int E, int N, int K,
+                                    int dtype, int out_dtype, void* dx, void* ws, size_t ws_bytes,
+                                    moe_stream_t stream);
+size_t moe_grouped_gemm_wgrad_workspace_size(int N);
+moe_status_t moe_grouped_gemm_wgrad(const void* dy, const void* x, const int32_t* offsets, int M, int E, int N, int K,
+                                    int dtype, float* dw, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * Newton-Schulz orthogonalisation of a batch of matrices (training): turns the gradient, or the
+ * momentum, of every expert's weight into the update of an optimiser that steps along the nearest
+ * semi-orthogonal matrix.  For each matrix g [M, N] of the batch
+ *   X = g / ||g||_F (0 for a zero matrix), then `steps` times
+ *   X <- a X + (b A + c A A) X,  A = X X^T,  (a, b, c) = (3.4445, -4.7750, 2.0315)
+ *   g    [B, M, N]  fp32 or bf16 (g_dtype), e.g. dw of moe_grouped_gemm_wgrad, or dgate_up of
+ *                   moe_layer_backward seen as [2E, F, D]
+ *   out  [B, M, N]  bf16 (must not overlap g)
+ * Computed in fp16 with a low-order part of X and fp32 accumulation; the result is rounded to bf16
+ * once and is within bf16's rounding of the exact iterate in the 2-norm.  A matrix that holds a NaN or
+ * an infinity comes out as NaN; the others of the batch are not affected.  Any sizes 1 <= M, N <=
+ * 65536, odd ones too; B >= 0; 1 <= steps <= 16 (5 is usual).
+ *   ws: as for moe_grouped_gemm; it holds a few matrices at a time, not the batch.
+ * ---------------------------------------------------------------------------------------- */
+size_t moe_orthogonalize_workspace_size(int B, int M, int N); /* 0 if a size is invalid */
+moe_status_t moe_orthogonalize(const void* g, int g_dtype, int B, int M, int N, int steps, moe_bf16_t* out, void* ws,
+                               size_t ws_bytes, moe_stream_t stream);
+
 /* Device address of the per-expert loads counts[E] (int32) that moe_layer_forward leaves in
  * its workspace (valid once the forward has run on the stream, until the next forward).  Host
  * call only: nothing is launched. */

@@ -25,6 +25,7 @@ MOE_PATH_STREAMING, MOE_PATH_FP8_STREAMING, MOE_PATH_ROW_TILES, MOE_PATH_WIDE_TI
 MOE_PATH_PAIR_TILES = 5
 MOE_WEIGHTS_BF16 = 0
 MOE_WEIGHTS_FP8_E4M3 = 1
+MOE_DTYPE_BF16, MOE_DTYPE_FP16, MOE_DTYPE_FP32 = 0, 1, 2
 
 STATUS = {
     0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHAPE", 3: "MOE_ERR_ALIGNMENT",
@@ -40,7 +41,9 @@ EXPORTS = (
     "moe_grouped_swiglu_ffn", "moe_combine", "moe_layer_workspace_size", "moe_layer_forward",
     "moe_layer_forward_host", "moe_layer_forward_timed", "moe_layer_kernel_count", "moe_layer_gemm_path", "moe_update_router_bias",
     "moe_layer_expert_counts", "moe_get_device_error", "moe_layer_backward_workspace_size", "moe_layer_backward",
-    "moe_status_string",
+    "moe_grouped_gemm_workspace_size", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
+    "moe_grouped_gemm_wgrad_workspace_size", "moe_grouped_gemm_wgrad", "moe_orthogonalize_workspace_size",
+    "moe_orthogonalize", "moe_status_string",
 )
 
 
@@ -104,6 +107,13 @@ def lib():
             "moe_get_device_error": ([P, P], I),
             "moe_layer_backward_workspace_size": ([ctypes.POINTER(LayerDesc)], Z),
             "moe_layer_backward": ([ctypes.POINTER(LayerDesc), P, P, P, ctypes.POINTER(LayerGrads), P, Z, P, Z, P], I),
+            "moe_grouped_gemm_workspace_size": ([I], Z),
+            "moe_grouped_gemm": ([P, P, P, I, I, I, I, I, I, P, P, Z, P], I),
+            "moe_grouped_gemm_dgrad": ([P, P, P, I, I, I, I, I, I, P, P, Z, P], I),
+            "moe_grouped_gemm_wgrad_workspace_size": ([I], Z),
+            "moe_grouped_gemm_wgrad": ([P, P, P, I, I, I, I, I, P, P, Z, P], I),
+            "moe_orthogonalize_workspace_size": ([I, I, I], Z),
+            "moe_orthogonalize": ([P, I, I, I, I, I, P, P, Z, P], I),
             "moe_status_string": ([I], ctypes.c_char_p),
         }
         for name, (args, res) in sig.items():
@@ -286,6 +296,137 @@ def moe_combine(out_perm, inv_perm, shared_out, T, k, y=None, stream=None):
     _check(lib().moe_combine(out_perm.data_ptr(), inv_perm.data_ptr(), _ptr(shared_out), T, D, k, y.data_ptr(),
                              _stream(stream)), "moe_combine")
     return y
+
+
+# ------------------------------------------------------------------------------ grouped products
+def _dtype_code(dtype):
+    import torch
+
+    return {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16, torch.float32: MOE_DTYPE_FP32}[dtype]
+
+
+def _need_on(t, device, name):
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+
+
+def _product_ws(ws, need, device):
+    """``ws`` if it is large enough, else a zero-filled workspace of ``need`` bytes."""
+    import torch
+
+    if ws is None or ws.numel() < need:
+        return torch.zeros(need, dtype=torch.uint8, device=device)
+    _need(ws, torch.uint8, None, "ws")
+    _need_on(ws, device, "ws")
+    return ws
+
+
+def _on_device(device, stream):
+    """(a context that makes ``device`` current, the handle of ``stream`` or of its current stream)."""
+    import torch
+
+    return torch.cuda.device(device), (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _rows_product(name, rows, offsets, w, contracted, wide, out, out_dtype, ws, stream):
+    import torch
+
+    if rows.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"expected bfloat16 or float16 rows, got {rows.dtype}")
+    if rows.dim() != 2 or w.dim() != 3:
+        raise ValueError("expected rows [M, .] and w [E, N, K]")
+    E, N, K = w.shape
+    M = rows.shape[0]
+    _need(rows, rows.dtype, (M, w.shape[contracted]), "x" if contracted == 2 else "dy")
+    _need(w, rows.dtype, None, "w")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    out_dtype = out_dtype or (rows.dtype if out is None else out.dtype)
+    if out_dtype not in (rows.dtype, torch.float32):
+        raise ValueError(f"out_dtype: expected {rows.dtype} or torch.float32, got {out_dtype}")
+    if out is None:
+        out = torch.empty(M, w.shape[wide], dtype=out_dtype, device=rows.device)
+    _need(out, out_dtype, (M, w.shape[wide]), "out")
+    for t, n in ((w, "w"), (offsets, "offsets"), (out, "out")):
+        _need_on(t, rows.device, n)
+    ws = _product_ws(ws, lib().moe_grouped_gemm_workspace_size(M), rows.device)
+    device, handle = _on_device(rows.device, stream)
+    with device:
+        _check(getattr(lib(), name)(rows.data_ptr(), offsets.data_ptr(), w.data_ptr(), M, E, N, K,
+                                    _dtype_code(rows.dtype), _dtype_code(out_dtype), out.data_ptr(), ws.data_ptr(),
+                                    ws.numel(), handle), name)
+    return out, ws
+
+
+def moe_grouped_gemm(x, offsets, w, out=None, out_dtype=None, ws=None, stream=None):
+    """y[r] = x[r] @ w[e].T for the rows r of each expert segment e: x [M, K], w [E, N, K] (both bf16 or
+    both fp16), offsets [E+1] int32 -> (y [M, N] in x's type or ``out_dtype`` = torch.float32, ws).
+    Rows of ``out`` outside every segment are left as they were.  Pass the returned ws (a zero-filled
+    workspace) to later calls to keep it."""
+    return _rows_product("moe_grouped_gemm", x, offsets, w, 2, 1, out, out_dtype, ws, stream)
+
+
+def moe_grouped_gemm_dgrad(dy, offsets, w, out=None, out_dtype=None, ws=None, stream=None):
+    """The input gradient of moe_grouped_gemm: dx[r] = dy[r] @ w[e], dy [M, N] -> (dx [M, K], ws)."""
+    return _rows_product("moe_grouped_gemm_dgrad", dy, offsets, w, 1, 2, out, out_dtype, ws, stream)
+
+
+def moe_grouped_gemm_wgrad(dy, x, offsets, out=None, ws=None, stream=None):
+    """The weight gradient of moe_grouped_gemm: dw[e] = dy_e.T @ x_e over the rows of segment e,
+    dy [M, N], x [M, K] -> (dw [E, N, K] fp32, ws); zeros for an expert without rows."""
+    import torch
+
+    if dy.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"expected bfloat16 or float16 rows, got {dy.dtype}")
+    if dy.dim() != 2 or x.dim() != 2 or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("expected dy [M, N], x [M, K] and offsets [E+1]")
+    M, N = dy.shape
+    K, E = x.shape[1], offsets.numel() - 1
+    _need(dy, dy.dtype, None, "dy")
+    _need(x, dy.dtype, (M, K), "x")
+    _need(offsets, torch.int32, None, "offsets")
+    if out is None:
+        out = torch.empty(E, N, K, dtype=torch.float32, device=dy.device)
+    _need(out, torch.float32, (E, N, K), "out")
+    for t, n in ((x, "x"), (offsets, "offsets"), (out, "out")):
+        _need_on(t, dy.device, n)
+    ws = _product_ws(ws, lib().moe_grouped_gemm_wgrad_workspace_size(N), dy.device)
+    device, handle = _on_device(dy.device, stream)
+    with device:
+        _check(lib().moe_grouped_gemm_wgrad(dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), M, E, N, K,
+                                            _dtype_code(dy.dtype), out.data_ptr(), ws.data_ptr(), ws.numel(), handle),
+               "moe_grouped_gemm_wgrad")
+    return out, ws
+
+
+def moe_orthogonalize(g, steps=5, out=None, ws=None, stream=None):
+    """The Newton-Schulz iterate of each matrix of g [..., M, N] (fp32 or bf16): X = g / ||g||_F, then
+    ``steps`` times X <- a X + (b A + c A A) X with A = X X^T -> (bf16 [..., M, N], ws).  Zero matrices
+    stay zero.  Typical g: the weight gradients of moe_grouped_gemm_wgrad, or the layer backward's
+    dgate_up.view(2 * E, F, D) and ddown."""
+    import torch
+
+    if g.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"g: expected float32 or bfloat16, got {g.dtype}")
+    if g.dim() < 2:
+        raise ValueError("g: expected [..., M, N]")
+    _need(g, g.dtype, None, "g")
+    M, N = g.shape[-2:]
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    _need(out, torch.bfloat16, tuple(g.shape), "out")
+    _need_on(out, g.device, "out")
+    B = g.numel() // (M * N) if M * N else 0
+    if B == 0:
+        return out, ws
+    need = lib().moe_orthogonalize_workspace_size(B, M, N)
+    if need == 0:
+        raise MoeError(2, "moe_orthogonalize_workspace_size")
+    ws = _product_ws(ws, need, g.device)
+    device, handle = _on_device(g.device, stream)
+    with device:
+        _check(lib().moe_orthogonalize(g.data_ptr(), _dtype_code(g.dtype), B, M, N, int(steps), out.data_ptr(),
+                                       ws.data_ptr(), ws.numel(), handle), "moe_orthogonalize")
+    return out, ws
 
 
 # ------------------------------------------------------------------------------ whole layer
