@@ -58,6 +58,7 @@ moe_status_t rows_product(const void* x, const int32_t* offsets, const void* w, 
   p.cols = W_MN ? K : N;
   p.K = W_MN ? N : K;
   p.kb_typ = (p.K + kBK - 1) / kBK;
+  p.rows_typ = M / E;  // the mean segment
   p.out = out;
   p.out_bf16 = dtype == MOE_DTYPE_BF16;
   p.withhold_first_load = test_withhold_this_launch() ? 1 : 0;
@@ -108,6 +109,7 @@ moe_status_t moe_grouped_gemm_wgrad(const void* dy, const void* x, const int32_t
   p.rows = N;
   p.cols = K;
   p.kb_typ = (M / E + kBK - 1) / kBK;  // the mean segment
+  p.rows_typ = N;
   p.out = dw;
   p.withhold_first_load = test_withhold_this_launch() ? 1 : 0;
   set_workspace(p, ws, partial_rows(N));

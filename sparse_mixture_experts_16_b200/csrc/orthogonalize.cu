@@ -33,7 +33,7 @@ namespace {
 
 constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
 constexpr float kScale = 4096.0f, kUnscale = 1.0f / 4096.0f;
-constexpr int kNormParts = 64;
+constexpr int kNormParts = 128;
 constexpr int kPrepThreads = 256;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -45,18 +45,46 @@ __device__ __forceinline__ float load_value<float>(const float* p) { return __ld
 template <>
 __device__ __forceinline__ float load_value<uint16_t>(const uint16_t* p) { return __uint_as_float((uint32_t)__ldg(p) << 16); }
 
-// partial[matrix][part] = sum of squares of the part's elements, in 64 bits and a fixed order
+// eight values from p, which is 16-byte aligned
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+// the first n of eight values from any p, zeros for the others
 template <typename T>
-__global__ void __launch_bounds__(kPrepThreads) norm_kernel(const T* __restrict__ g, long long count,
+__device__ __forceinline__ void load8_tail(const T* p, int n, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = i < n ? load_value(p + i) : 0.0f;
+}
+
+// partial[matrix][part] = sum of squares of the part's elements, in 64 bits and a fixed order.  Bound by
+// reading g once; `wide`: every matrix starts on 16 bytes.
+template <typename T>
+__global__ void __launch_bounds__(kPrepThreads) norm_kernel(const T* __restrict__ g, long long count, int wide,
                                                             double* __restrict__ partial) {
   __shared__ double warp_sum[kPrepThreads / 32];
   pdl_wait();
   pdl_trigger();
   const T* m = g + (long long)blockIdx.y * count;
+  const long long groups = (count + 7) / 8;
   double sum = 0.0;
-  for (long long i = (long long)blockIdx.x * kPrepThreads + threadIdx.x; i < count; i += (long long)gridDim.x * kPrepThreads) {
-    const double v = load_value(m + i);
-    sum += v * v;
+#pragma unroll 4
+  for (long long i = (long long)blockIdx.x * kPrepThreads + threadIdx.x; i < groups; i += (long long)gridDim.x * kPrepThreads) {
+    float v[8];
+    const long long left = count - 8 * i;
+    if (wide && left >= 8) load8(m + 8 * i, v);
+    else load8_tail(m + 8 * i, left < 8 ? (int)left : 8, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += (double)v[j] * (double)v[j];
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -69,30 +97,49 @@ __global__ void __launch_bounds__(kPrepThreads) norm_kernel(const T* __restrict_
   }
 }
 
-// hi + lo * 2^-11 = 2^12 g / ||g||, rows padded with zeros to the pitch
+// hi + lo * 2^-11 = 2^12 g / ||g||, rows padded with zeros to the pitch; bound by reading g and writing
+// as many bytes.  `wide`: every row of g starts on 16 bytes.
 template <typename T>
-__global__ void __launch_bounds__(kPrepThreads) scale_kernel(const T* __restrict__ g, int M, int N, int ld,
+__global__ void __launch_bounds__(kPrepThreads) scale_kernel(const T* __restrict__ g, int M, int N, int ld, int wide,
                                                              const double* __restrict__ partial, int parts,
                                                              uint16_t* __restrict__ hi, uint16_t* __restrict__ lo) {
   __shared__ double inv;
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < 32) {
     double t = 0.0;
-    for (int i = 0; i < parts; ++i) t += partial[(size_t)blockIdx.y * kNormParts + i];
-    inv = t == 0.0 ? 0.0 : (double)kScale / sqrt(t);
+    for (int i = threadIdx.x; i < parts; i += 32) t += partial[(size_t)blockIdx.y * kNormParts + i];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+    if (threadIdx.x == 0) inv = t == 0.0 ? 0.0 : (double)kScale / sqrt(t);
   }
   __syncthreads();
   const double f = inv;
   const T* m = g + (long long)blockIdx.y * M * N;
   const long long base = (long long)blockIdx.y * M * ld;
-  const long long total = (long long)M * ld;
-  for (long long i = (long long)blockIdx.x * kPrepThreads + threadIdx.x; i < total; i += (long long)gridDim.x * kPrepThreads) {
-    const int r = (int)(i / ld), c = (int)(i - (long long)r * ld);
-    const float v = c < N ? (float)((double)load_value(m + (long long)r * N + c) * f) : 0.0f;
-    const uint16_t h = half_bits(v);
-    hi[base + i] = h;
-    lo[base + i] = half_bits((v - half_val(h)) * 2048.0f);
+  const unsigned per = (unsigned)ld / 8;  // groups of 8 per row
+  const unsigned groups = (unsigned)M * per;
+#pragma unroll 2
+  for (unsigned i = blockIdx.x * kPrepThreads + threadIdx.x; i < groups; i += gridDim.x * kPrepThreads) {
+    const unsigned r = i / per, c = (i - r * per) * 8;
+    const T* at = m + (long long)r * N + c;
+    float v[8];
+    if (wide) load8(at, v);
+    else load8_tail(at, min(8, N - (int)c), v);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[j] = 0, l[j] = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float w = (float)((double)v[2 * j + u] * f);
+        const uint16_t hb = half_bits(w);
+        h[j] |= (uint32_t)hb << 16 * u;
+        l[j] |= (uint32_t)half_bits((w - half_val(hb)) * 2048.0f) << 16 * u;
+      }
+    }
+    *reinterpret_cast<uint4*>(hi + base + 8LL * i) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(lo + base + 8LL * i) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 
@@ -103,18 +150,22 @@ struct Layout {
   size_t norms, hi0, hi1, lo, gram, poly, total;
 };
 
-// Enough matrices side by side to fill several rounds of clusters with X's tiles, no more: what is in
-// flight then stays small next to memory, and for small matrices in L2.
-constexpr int kTargetTiles = 592;  // 8 rounds of 74 clusters
+// Enough matrices side by side that the launch with the fewest tiles, the Gram matrix's, fills four rounds
+// of 74 clusters, within 1 GB of X; dealt evenly over the rounds of launches.
+constexpr long long kTargetTiles = 296;
+constexpr long long kBatchBytes = 1LL << 30;
 
 bool layout_of(int B, int M, int N, Layout& l) {
   if (B <= 0 || M <= 0 || N <= 0 || M > 65536 || N > 65536) return false;
   l.low = M < N ? M : N;
   l.lp = (l.low + 7) / 8 * 8;
   l.np = (N + 7) / 8 * 8;
-  const long long tiles = (long long)((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
-  const long long batch = (kTargetTiles + tiles - 1) / tiles;
-  l.batch = B < batch ? B : (int)batch;
+  const long long rt = (l.low + kTile - 1) / kTile, tiles = rt * (rt + 1) / 2;
+  long long batch = (kTargetTiles + tiles - 1) / tiles;
+  const long long fits = kBatchBytes / (6LL * M * l.np);
+  if (batch > fits) batch = fits > 1 ? fits : 1;
+  const long long rounds = (B + batch - 1) / batch;
+  l.batch = (int)((B + rounds - 1) / rounds);
   l.prows = partial_rows(M);
   size_t at = align_up(kPartialOffset + partial_bytes(l.prows), 256);
   auto take = [&](size_t bytes) {
@@ -139,12 +190,15 @@ cudaError_t prepare(const T* g, int count, int M, int N, const Layout& l, uint8_
   long long parts = (n + 16 * kPrepThreads - 1) / (16 * kPrepThreads);
   if (parts > kNormParts) parts = kNormParts;
   double* norms = reinterpret_cast<double*>(b + l.norms);
-  cudaError_t e = launch_pdl(norm_kernel<T>, dim3((unsigned)parts, (unsigned)count), dim3(kPrepThreads), 0, s, g, n, norms);
+  // g is on 16 bytes: so is every matrix, or every row, whose length is a multiple of 16 bytes
+  const int unit = 16 / (int)sizeof(T);
+  cudaError_t e = launch_pdl(norm_kernel<T>, dim3((unsigned)parts, (unsigned)count), dim3(kPrepThreads), 0, s, g, n,
+                             n % unit == 0 ? 1 : 0, norms);
   if (e != cudaSuccess) return e;
-  long long blocks = ((long long)M * l.np + 8 * kPrepThreads - 1) / (8 * kPrepThreads);
+  long long blocks = ((long long)M * (l.np / 8) + 2 * kPrepThreads - 1) / (2 * kPrepThreads);
   if (blocks > 1024) blocks = 1024;
   return launch_pdl(scale_kernel<T>, dim3((unsigned)blocks, (unsigned)count), dim3(kPrepThreads), 0, s, g, M, N, l.np,
-                    (const double*)norms, (int)parts, reinterpret_cast<uint16_t*>(b + l.hi0),
+                    N % 8 == 0 ? 1 : 0, (const double*)norms, (int)parts, reinterpret_cast<uint16_t*>(b + l.hi0),
                     reinterpret_cast<uint16_t*>(b + l.lo));
 }
 
@@ -159,7 +213,8 @@ cudaError_t iterate(int count, int M, int N, int steps, const Layout& l, uint16_
   base.counters = reinterpret_cast<int*>(b + kWsHeader);
   base.partial = reinterpret_cast<float*>(b + kPartialOffset);
   base.prows = l.prows;
-  base.src_lo = base.out_lo = reinterpret_cast<uint16_t*>(b + l.lo);
+  const OperandHost olo = {b + l.lo, (uint64_t)l.np, (uint64_t)M, G};
+  if (!set_chunks(&base.src_lo_map, olo) || !set_chunks(&base.out_lo_map, olo)) return cudaErrorInvalidValue;
   uint16_t* hi[2] = {reinterpret_cast<uint16_t*>(b + l.hi0), reinterpret_cast<uint16_t*>(b + l.hi1)};
   uint16_t* gram = reinterpret_cast<uint16_t*>(b + l.gram);
   uint16_t* poly = reinterpret_cast<uint16_t*>(b + l.poly);
@@ -176,6 +231,7 @@ cudaError_t iterate(int count, int M, int N, int steps, const Layout& l, uint16_
     p.ld = l.lp;
     p.K = tall ? M : l.np;
     p.kb_typ = (p.K + kBK - 1) / kBK;
+    p.rows_typ = l.low;
     p.out = gram;
     p.c1 = kUnscale;
     if (tall) {
@@ -192,8 +248,9 @@ cudaError_t iterate(int count, int M, int N, int steps, const Layout& l, uint16_
     p.ld = l.lp;
     p.K = l.lp;
     p.kb_typ = (p.K + kBK - 1) / kBK;
-    p.src = gram;
+    p.rows_typ = l.low;
     p.out = poly;
+    if (!set_chunks(&p.src_map, og) || !set_chunks(&p.out_map, op)) return cudaErrorInvalidValue;
     p.c0 = kNsB;
     p.c1 = kNsC * kUnscale;
     if (!set_operands<false, false>(p, og, og, false)) return cudaErrorInvalidValue;
@@ -205,9 +262,13 @@ cudaError_t iterate(int count, int M, int N, int steps, const Layout& l, uint16_
     p.ld = l.np;
     p.K = l.lp;
     p.kb_typ = (p.K + kBK - 1) / kBK;
-    p.src = hi[k & 1];
+    p.rows_typ = M;
     p.out = last ? out : hi[(k + 1) & 1];
-    p.ld_out = p.cols_out = N;
+    p.cols_out = N;
+    p.store_out = N % 8 == 0 ? 1 : 0;
+    const OperandHost onext = {p.out, (uint64_t)(last ? N : l.np), (uint64_t)M, G};
+    if (!set_chunks(&p.src_map, ox)) return cudaErrorInvalidValue;
+    if ((!last || p.store_out) && !set_chunks(&p.out_map, onext)) return cudaErrorInvalidValue;
     p.c0 = kNsA;
     p.c1 = kUnscale;
     p.c2 = kUnscale;

@@ -16,10 +16,11 @@
 // 128 x 256 x 64 product -- 64 bytes per cycle and SM at the tensor pipe's rate, where a one-CTA tile
 // would need 96.  No load is multicast.
 //
-// Kernel layout (persistent clusters of two, 320 threads per CTA):
+// Kernel layout (persistent clusters of two, 352 threads per CTA):
 //   warp 0     TMA producer: 6 stages of 32 KB.
 //   warp 1     TMEM allocation; in the even CTA one thread issues the pair's MMAs.
 //   warps 2-9  epilogue: four TMEM lane quarters x two halves of the rows.
+//   warp 10    ragged K: clears the rows behind a segment in its last K block.
 // Tiles are dealt round-robin.  The tiles of the last, partly filled round are split along K when
 // that shortens the round (few rows, one token: split_of); each part stores its fp32 accumulators and
 // the last part to arrive (an atomic counter per warp's share, no waiting) adds them in the order of
@@ -61,17 +62,23 @@ enum Epilogue {
 
 constexpr int kTile = 256;               // rows (N) and columns (M) of a pair's tile
 constexpr int kBK = 64;                  // K per stage
-constexpr int kStages = 6;
-constexpr int kThreads = 320;
+constexpr int kStages = 6;               // 5 where the epilogue stages 16-bit tiles (stages_of)
+constexpr int kThreads = 352;
 constexpr int kEpiWarps = 8;
 constexpr int kTileA = 128 * kBK * 2;    // 16 KB: this CTA's columns
 constexpr int kTileB = 128 * kBK * 2;    // 16 KB: this CTA's rows, at most
 constexpr int kStageBytes = kTileA + kTileB;
 constexpr int kPromoteBlocks = 8;        // K blocks per accumulator drain (512 k)
 constexpr int kMaxGroups = 1024;
-constexpr int kBarBytes = 256;
-constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kBarBytes + 4 * (kMaxGroups + 4);
-static_assert(kSmemBytes <= 232448, "shared memory budget");
+constexpr int kBarBytes = 384;  // 3 per stage, 4 of the accumulators, 16 of the staging, the tensor memory's address
+constexpr int kChunkBytes = 32 * 32 * 2;  // 32 rows x 32 columns of 16 bits: what a warp's epilogue handles at a time
+constexpr int kStagingBytes = kEpiWarps * 2 * 2 * kChunkBytes;  // two buffers of two arrays per warp
+constexpr bool staged(int epi) { return epi == kPoly || epi == kApply || epi == kApplyLast; }
+constexpr int stages_of(int epi) { return staged(epi) ? kStages - 1 : kStages; }
+constexpr size_t smem_bytes(int epi) {
+  return 1024 + (size_t)stages_of(epi) * kStageBytes + kBarBytes + (staged(epi) ? kStagingBytes + 16 : 4 * (kMaxGroups + 4));
+}
+static_assert(smem_bytes(kOut32) <= 232448 && smem_bytes(kApply) <= 232448, "shared memory budget");
 
 // workspace of a launch: error word, counters (zero between launches), split-K partial sums
 constexpr int kMaxParts = 148;           // split tiles x parts
@@ -81,28 +88,35 @@ constexpr size_t kPartialOffset = kWsHeader + kCounterBytes;
 inline int partial_rows(long long rows) { return rows >= kTile ? kTile : (int)((rows + 31) / 32 * 32); }
 inline size_t partial_bytes(int prows) { return (size_t)kMaxParts * 2 * 128 * 4 * (size_t)prows; }
 
+// Boxes of a K-major B: a tile's rows come in one request of the smallest box that holds half of them.
+// The rows behind them are loaded for nothing, which costs less than exact boxes: four requests of
+// 32 + 32 + 32 + 8 rows took a product of 1040 rows per segment from 923 to 1246 us.
+constexpr int kBoxes = 5;
+__host__ __device__ constexpr int box_rows(int i) { return i == 0 ? 128 : i == 1 ? 96 : i == 2 ? 64 : i == 3 ? 32 : 8; }
+__device__ __forceinline__ int box_of(int half) { return half > 96 ? 0 : half > 64 ? 1 : half > 32 ? 2 : half > 8 ? 3 : 4; }
+
 struct alignas(64) Params {
-  CUtensorMap a;    // K-major: box 64 k x 128 columns; MN-major: box 64 columns x 64 k
-  CUtensorMap b;    // K-major: box 64 k x 128 rows;    MN-major: box 64 rows x 64 k
-  CUtensorMap b32;  // K-major only: the same tensor, boxes of 32 and 8 rows for ragged halves
-  CUtensorMap b8;
+  CUtensorMap a;          // K-major: box 64 k x 128 columns; MN-major: box 64 columns x 64 k
+  CUtensorMap b[kBoxes];  // K-major: boxes of 64 k x box_rows(i) rows; MN-major (the first): 64 rows x 64 k
   const int32_t* offsets;  // kRaggedRows / kRaggedK: segment bounds [G + 1]
+  CUtensorMap src_map;     // staged epilogues: src, src_lo, out, out_lo in boxes of 32 columns x 32 rows
+  CUtensorMap src_lo_map;
+  CUtensorMap out_map;
+  CUtensorMap out_lo_map;
+  int store_out;           // kApplyLast: out_map holds out (its pitch allows it)
   int G;                   // groups
   int M_total;             // rows of the ragged tensor
   int rows, cols, K;       // rows (not kRaggedRows), columns and K (not kRaggedK) of a group
   uint32_t idesc;          // instruction descriptor without M and N
   int out_bf16;            // kOut16: bf16 instead of fp16
-  int ld, ld_out;          // row pitch of src / src_lo / out / out_lo; of the last output
-  int cols_out;            // kApplyLast: columns that are stored
+  int ld;                  // row pitch of src / out of the Newton-Schulz epilogues
+  int cols_out;            // kApplyLast: row pitch of out, columns that are stored
   void* out;
-  uint16_t* out_lo;
-  const uint16_t* src;
-  const uint16_t* src_lo;
   float c0, c1, c2;
   float* partial;
   int* counters;
   int prows;               // rows per partial tile
-  int kb_typ;              // K blocks of a typical tile (the split's cost model)
+  int kb_typ, rows_typ;    // K blocks and rows of a typical tile (the split's cost model)
   int withhold_first_load; // test only: the even CTA never issues its first stage's copies
   int* err;
 };
@@ -146,6 +160,17 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
   return true;
 }
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// generic accesses of shared memory before -> the TMA's or the tensor core's after
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // UMMA descriptor of an MN-major operand: 64-element chunks 8 KB apart, 8-k groups 1 KB apart
 __device__ __forceinline__ uint64_t mn_desc(uint32_t addr) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
@@ -159,18 +184,20 @@ struct Sched {
   int items;
 };
 
-// Parts of each of the r < clusters tiles of the last round.  Cost in K blocks: rounds of parts, each
-// with a fixed share for filling the pipeline and for the epilogue, and the reading of the parts.
-// Without the split a one-token product of 4 experts x [5760, 2880] leaves 3/4 of the clusters idle in
-// its second round.
-__device__ __forceinline__ int split_of(int r, int clusters, int kb) {
+// Parts of each of the r < clusters tiles of the last round.  Cost in K blocks (of about 0.3 us): rounds
+// of parts, each with a fixed share for filling the pipeline and for the epilogue; then the parts' way
+// through memory, 16 rows x 4 parts at a time, a memory latency or two K blocks each.  Without the split
+// a one-token product of 4 experts x [5760, 2880] leaves 3/4 of the clusters idle in its second round;
+// full tiles of 256 rows are worth splitting only along a long K.
+__device__ __forceinline__ int split_of(int r, int clusters, int kb, int rows) {
   if (r <= 0) return 1;
   const int most = min(kMaxSplit, min(kb / 2, kMaxParts / r));
+  const float groups = (float)((min(rows, 128) + 15) / 16);
   int best = 1;
   float cost = 1e30f;
   for (int s = 1; s <= most || s == 1; ++s) {
     const float rounds = (float)((r * s + clusters - 1) / clusters);
-    const float c = rounds * ((float)kb / (float)s + 4.0f) + (s > 1 ? 2.0f + 0.5f * (float)s : 0.0f);
+    const float c = rounds * ((float)kb / (float)s + 4.0f) + (s > 1 ? 4.0f + 2.0f * groups * (float)((s + 3) / 4) : 0.0f);
     if (c < cost) cost = c, best = s;
   }
   return best;
@@ -179,7 +206,7 @@ __device__ __forceinline__ int split_of(int r, int clusters, int kb) {
 struct Item {
   int g;
   int rt, ct;        // row tile, column tile
-  int nr;            // rows of this tile (1..256)
+  int r0, nr;        // rows of this tile within the group: [r0, r0 + nr), nr = 1..256
   int row0;          // kRaggedRows: first row of the segment
   int k0, krows;     // kRaggedK: first k row and number of k rows
   int kb0, kb1;      // K blocks [kb0, kb1)
@@ -250,28 +277,51 @@ __device__ __forceinline__ Item item_of(const Params& p, const int* tile_start, 
     x.ct = rem / rb;
     x.rt = 8 * band + (rem - x.ct * rb);
   }
-  x.nr = min(kTile, rows - x.rt * kTile);
+  // Rows are dealt evenly over the tiles, in 16s: a tile of few rows costs nearly half a full one, for
+  // the columns' operand comes in whole.  The symmetric products keep square tiles, and what leaves in
+  // boxes of 32 rows tiles of whole boxes.
+  constexpr int kUnit = staged(EPI) ? 32 : 16;
+  const int step = EPI == kGram || EPI == kPoly ? kTile : ((rows + rt - 1) / rt + kUnit - 1) / kUnit * kUnit;
+  x.r0 = x.rt * step;
+  x.nr = min(step, rows - x.r0);
   const int kb = RAGGED == kRaggedK ? (x.krows + kBK - 1) / kBK : (p.K + kBK - 1) / kBK;
   x.kb0 = split_begin(kb, x.part, parts);
   x.kb1 = split_end(kb, x.part, parts);
   return x;
 }
 
-// rows of B each CTA holds: half of the tile's rows rounded up to 16 (an MN-major B: always 128, the
-// rows past the tensor read as zero)
-template <bool B_MN>
-__device__ __forceinline__ int half_of(int nr) {
-  return B_MN ? 128 : ((nr + 15) / 16) * 8;
-}
+// rows of B each CTA multiplies: half of the tile's rows rounded up to 16
+__device__ __forceinline__ int half_of(int nr) { return ((nr + 15) / 16) * 8; }
+
+// kRaggedK: the K block at kx ends behind the segment and inside a 16-long instruction
+__device__ __forceinline__ bool ragged_tail(int krows, int kx) { return kx + kBK > krows && ((krows - kx) & 15) != 0; }
 
 // ------------------------------------------------------------------------------ epilogue
 __device__ __forceinline__ uint16_t half_bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
 __device__ __forceinline__ float half_val(uint16_t b) { return __half2float(__ushort_as_half(b)); }
 
-// v[j] = accumulator of row j0 + j and column col (this lane's) of the item; nj rows are valid
+// Symmetric products: h[j], the values of rows row_in + j and column col, as row col, columns row_in + j
+__device__ __forceinline__ void mirror(const Params& p, const Item& x, const uint16_t (&h)[32], int row_in, int col) {
+  if (x.rt == x.ct || col >= p.rows) return;
+  uint16_t* m = static_cast<uint16_t*>(p.out) + ((long long)x.g * p.rows + col) * p.ld + row_in;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (row_in + 8 * u + 8 <= p.ld) {
+      uint4 w;
+      w.x = (uint32_t)h[8 * u] | (uint32_t)h[8 * u + 1] << 16;
+      w.y = (uint32_t)h[8 * u + 2] | (uint32_t)h[8 * u + 3] << 16;
+      w.z = (uint32_t)h[8 * u + 4] | (uint32_t)h[8 * u + 5] << 16;
+      w.w = (uint32_t)h[8 * u + 6] | (uint32_t)h[8 * u + 7] << 16;
+      *reinterpret_cast<uint4*>(m + 8 * u) = w;
+    }
+  }
+}
+
+// One warp's 32 rows x 32 columns, v[j] = accumulator of row j0 + j and column col (this lane's); nj rows
+// are valid.  A row of 32 columns is one store of a warp.
 template <int RAGGED, int EPI>
 __device__ __forceinline__ void emit(const Params& p, const Item& x, const float (&v)[32], int j0, int nj, int col) {
-  const int row_in = x.rt * kTile + j0;  // row within the group
+  const int row_in = x.r0 + j0;  // row within the group
   const long long row = (RAGGED == kRaggedRows ? (long long)x.row0 : (long long)x.g * p.rows) + row_in;
   if constexpr (EPI == kOut16) {
     if (col >= p.cols) return;
@@ -290,49 +340,110 @@ __device__ __forceinline__ void emit(const Params& p, const Item& x, const float
 #pragma unroll
     for (int j = 0; j < 32; ++j)
       if (j < nj) o[(long long)j * p.cols] = v[j];
-  } else if constexpr (EPI == kGram || EPI == kPoly) {
+  } else {  // kGram
     uint16_t h[32];
-    const long long base = (long long)x.g * p.rows * p.ld;
-    const uint16_t* s = p.src + base + (long long)row_in * p.ld + col;
-    uint16_t* o = static_cast<uint16_t*>(p.out) + base + (long long)row_in * p.ld + col;
+    uint16_t* o = static_cast<uint16_t*>(p.out) + row * p.ld + col;
     const bool col_ok = col < p.ld;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      float w = v[j] * p.c1;
-      if constexpr (EPI == kPoly) w += (col_ok && j < nj) ? p.c0 * half_val(s[(long long)j * p.ld]) : 0.0f;
-      h[j] = half_bits(w);
+      h[j] = half_bits(v[j] * p.c1);
       if (col_ok && j < nj) o[(long long)j * p.ld] = h[j];
     }
-    if (x.rt != x.ct && col < p.rows) {  // the mirror image: row `col`, columns row_in ..
-      uint16_t* m = static_cast<uint16_t*>(p.out) + base + (long long)col * p.ld + row_in;
+    mirror(p, x, h, row_in, col);
+  }
+}
+
+// The staged epilogues' chunks.  What they add to the accumulators (src, and src_lo for X) comes by TMA
+// into one of the warp's two buffers, the result takes its place there and leaves by TMA, while the next
+// chunk's addends come into the other buffer.  (With two-byte loads and stores of the lanes the same
+// launch took 590 us instead of 430 on 8 matrices of 2048 x 7168, K = 2048; its MMAs take 300.)
+struct Staging {
+  uint8_t* buf;    // 2 x (2 KB of src and out, 2 KB of their low-order parts)
+  uint64_t* bar;   // 2: landed
+  uint32_t n;      // chunks fetched so far
+};
+
+// lane 0: fetch the chunk at (col0, row) into the next buffer, whose last store was the last but one
+template <int EPI>
+__device__ __forceinline__ void fetch(const Params& p, Staging& st, int g, int row, int col0, int lane) {
+  if (lane == 0) {
+    uint8_t* b = st.buf + (st.n & 1) * 2 * kChunkBytes;
+    uint64_t* bar = &st.bar[st.n & 1];
+    bulk_wait_read();
+    mbar_arrive_expect_tx(bar, EPI == kPoly ? kChunkBytes : 2 * kChunkBytes);
+    tma_3d(&p.src_map, bar, b, col0, row, g);
+    if constexpr (EPI != kPoly) tma_3d(&p.src_lo_map, bar, b + kChunkBytes, col0, row, g);
+  }
+  ++st.n;
+}
+
+// the chunk fetched `ago` fetches before the last one has landed (false: the wait expired); adds v, stores
+template <int EPI>
+__device__ __forceinline__ bool emit_staged(const Params& p, const Item& x, const Staging& st, int ago,
+                                            const float (&v)[32], int j0, int nj, int col, int lane) {
+  const uint32_t n = st.n - 1 - ago;
+  uint16_t* hi = reinterpret_cast<uint16_t*>(st.buf + (n & 1) * 2 * kChunkBytes) + lane;
+  uint16_t* lo = hi + kChunkBytes / 2;
+  if (!__all_sync(0xffffffffu, mbar_wait(&st.bar[n & 1], (n >> 1) & 1, kWaitLimitNs))) return false;
+  const int row = x.r0 + j0, col0 = col - lane;
+  if constexpr (EPI == kPoly) {
+    uint16_t h[32];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (row_in + 8 * u + 8 <= p.ld) {
-          uint4 w;
-          w.x = (uint32_t)h[8 * u] | (uint32_t)h[8 * u + 1] << 16;
-          w.y = (uint32_t)h[8 * u + 2] | (uint32_t)h[8 * u + 3] << 16;
-          w.z = (uint32_t)h[8 * u + 4] | (uint32_t)h[8 * u + 5] << 16;
-          w.w = (uint32_t)h[8 * u + 6] | (uint32_t)h[8 * u + 7] << 16;
-          *reinterpret_cast<uint4*>(m + 8 * u) = w;
+    for (int j = 0; j < 32; ++j) {
+      h[j] = half_bits(v[j] * p.c1 + p.c0 * half_val(hi[j * 32]));
+      hi[j * 32] = h[j];
+    }
+    mirror(p, x, h, row, col);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float w = p.c0 * (half_val(hi[j * 32]) + half_val(lo[j * 32]) * (1.0f / 2048.0f)) + v[j] * p.c1;
+      if constexpr (EPI == kApply) {
+        const uint16_t h = half_bits(w);
+        hi[j * 32] = h;
+        lo[j * 32] = half_bits((w - half_val(h)) * 2048.0f);
+      } else {
+        const uint16_t b = __bfloat16_as_ushort(__float2bfloat16_rn(w * p.c2));
+        if (p.store_out) {
+          hi[j * 32] = b;
+        } else if (j < nj && col < p.cols_out) {
+          static_cast<uint16_t*>(p.out)[((long long)x.g * p.rows + row + j) * p.cols_out + col] = b;
         }
       }
     }
-  } else {
-    if (col >= p.ld) return;
-    const long long at = row * p.ld + col;
+  }
+  fence_async();
+  __syncwarp();
+  if (lane == 0) {
+    uint8_t* b = st.buf + (n & 1) * 2 * kChunkBytes;
+    if (EPI != kApplyLast || p.store_out) tma_store_3d(&p.out_map, b, col0, row, x.g);
+    if constexpr (EPI == kApply) tma_store_3d(&p.out_lo_map, b + kChunkBytes, col0, row, x.g);
+    bulk_commit();
+  }
+  return true;
+}
+
+// the sum of a split tile's parts over rows j0 + [0, 32), in the order of the parts, ROWS x PARTS loads in
+// flight at a time (past the last row or part: the last again)
+template <int ROWS, int PARTS>
+__device__ __forceinline__ void add_parts(const float* first, size_t pitch, int parts, int nj, float (&v)[32]) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (j < nj) {
-        const long long i = at + (long long)j * p.ld;
-        const float w = p.c0 * (half_val(p.src[i]) + half_val(p.src_lo[i]) * (1.0f / 2048.0f)) + v[j] * p.c1;
-        if constexpr (EPI == kApply) {
-          const uint16_t h = half_bits(w);
-          static_cast<uint16_t*>(p.out)[i] = h;
-          p.out_lo[i] = half_bits((w - half_val(h)) * 2048.0f);
-        } else if (col < p.cols_out) {
-          static_cast<uint16_t*>(p.out)[(row + j) * p.ld_out + col] =
-              __bfloat16_as_ushort(__float2bfloat16_rn(w * p.c2));
-        }
+  for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 32; j += ROWS) {
+    if (j < nj) {
+#pragma unroll 1
+      for (int s = 0; s < parts; s += PARTS) {
+        float t[PARTS][ROWS];
+#pragma unroll
+        for (int u = 0; u < PARTS; ++u)
+#pragma unroll
+          for (int i = 0; i < ROWS; ++i)
+            t[u][i] = __ldcg(first + min(s + u, parts - 1) * pitch + (size_t)min(j + i, nj - 1) * 128);
+#pragma unroll
+        for (int u = 0; u < PARTS; ++u)
+#pragma unroll
+          for (int i = 0; i < ROWS; ++i) v[j + i] += s + u < parts && j + i < nj ? t[u][i] : 0.0f;
       }
     }
   }
@@ -345,7 +456,8 @@ __device__ __forceinline__ float* part_ptr(const Params& p, int slot, int split,
 // ------------------------------------------------------------------------------ the kernel
 template <bool A_MN, bool B_MN, int RAGGED, int EPI>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p) {
-  constexpr bool kPromote = EPI == kOut32;
+  constexpr bool kPromote = EPI == kOut32, kStaged = staged(EPI);
+  constexpr int kStages = stages_of(EPI);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);  // even CTA: both halves landed
@@ -353,8 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   uint64_t* acc_full = empty + kStages;                                       // both CTAs: accumulator ready
   uint64_t* acc_empty = acc_full + 2;                                         // even CTA: both epilogues done
   uint64_t* tail_bar = acc_empty + 2;                                         // kRaggedK: this CTA's tail block landed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail_bar + 1);
-  int* sched_smem = reinterpret_cast<int*>(smem + kStages * kStageBytes + kBarBytes);
+  uint64_t* staging_bar = tail_bar + kStages;                                 // staged: two per epilogue warp
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(staging_bar + 2 * kEpiWarps);
+  uint8_t* staging = smem + kStages * kStageBytes + kBarBytes;
+  int* sched_smem = reinterpret_cast<int*>(staging + (kStaged ? kStagingBytes : 0));
   int* tile_start = sched_smem + 3;  // kRaggedRows: [G + 1]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -364,21 +478,18 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], RAGGED == kRaggedK ? 2 : 1);  // kRaggedK: each CTA's producer arrives
+      mbar_init(&full[s], RAGGED == kRaggedK ? 2 : 1);  // kRaggedK: see the tail blocks below
       mbar_init(&empty[s], 1);
+      mbar_init(&tail_bar[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 2 * kEpiWarps);
     }
-    mbar_init(tail_bar, 1);
+    for (int b = 0; b < 2 * kEpiWarps; ++b) mbar_init(&staging_bar[b], 1);
     fence_barrier_init();
     prefetch_tensormap(&p.a);
-    prefetch_tensormap(&p.b);
-    if constexpr (!B_MN) {
-      prefetch_tensormap(&p.b32);
-      prefetch_tensormap(&p.b8);
-    }
+    for (int i = 0; i < (B_MN ? 1 : kBoxes); ++i) prefetch_tensormap(&p.b[i]);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 2 * kTile);
@@ -421,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     if (lane == 0) {
       const int r = total % n_clusters;
-      const int split = p.partial != nullptr ? split_of(r, n_clusters, p.kb_typ) : 1;
+      const int split = p.partial != nullptr ? split_of(r, n_clusters, p.kb_typ, p.rows_typ) : 1;
       sched_smem[0] = split > 1 ? total - r : total;
       sched_smem[1] = split;
       sched_smem[2] = split > 1 ? total - r + r * split : total;
@@ -436,22 +547,22 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer (both CTAs)
-    if (RAGGED == kRaggedK || lane == 0) {
-      uint32_t it = 0, tails = 0;
+    if (lane == 0) {
+      uint32_t it = 0;
       bool ok = true;
       for (int i = cluster_id; i < sc.items && ok; i += n_clusters) {
         const Item x = item_of<RAGGED, EPI>(p, tile_start, sc, i);
-        const int half = half_of<B_MN>(x.nr);
-        const uint32_t bytes = (uint32_t)kTileA + (uint32_t)half * 128u;
+        const int half = half_of(x.nr);
+        const int box = B_MN ? 0 : box_of(half);
+        const CUtensorMap* bmap = &p.b[box];
+        const uint32_t bytes = (uint32_t)kTileA + (B_MN ? (half > 64 ? 16384u : 8192u) : (uint32_t)box_rows(box) * 128u);
         const int acol = x.ct * kTile + (int)rank * 128;
-        const int brow = (RAGGED == kRaggedRows ? x.row0 : 0) + x.rt * kTile + (int)rank * half;
+        const int brow = (RAGGED == kRaggedRows ? x.row0 : 0) + x.r0 + (int)rank * half;
         const int ag = RAGGED == kRaggedK ? 0 : x.g;
         const int bg = RAGGED == kDense ? x.g : 0;
         for (int kb = x.kb0; kb < x.kb1; ++kb, ++it) {
           const int stage = it % kStages;
-          bool free_ = mbar_wait(&empty[stage], ((it / kStages) & 1) ^ 1, kWaitLimitNs);
-          if constexpr (RAGGED == kRaggedK) free_ = __all_sync(0xffffffffu, free_);
-          if (!free_) {
+          if (!mbar_wait(&empty[stage], ((it / kStages) & 1) ^ 1, kWaitLimitNs)) {
             ok = false;
             break;
           }
@@ -459,79 +570,44 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           uint8_t* sb = sa + kTileA;
           const int kx = kb * kBK;
           const int ky = x.k0 + kx;  // k as a row of an MN-major operand (x.k0 = 0 unless kRaggedK)
-          // kRaggedK: the rows of the last block past the segment belong to the next one
-          const bool tail = RAGGED == kRaggedK && kx + kBK > x.krows;
-          if (!tail) {
-            if (lane == 0) {
-              const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
-              if (leader) mbar_arrive_expect_tx(&full[stage], 2u * bytes);
-              else if (RAGGED == kRaggedK) mbar_arrive_cluster(bar);
-              if (!(leader && p.withhold_first_load && it == 0)) {
-                if constexpr (A_MN) {
-                  tma_3d_pair(&p.a, bar, sa, acol, ky, ag);
-                  tma_3d_pair(&p.a, bar, sa + 8192, acol + 64, ky, ag);
-                } else {
-                  tma_3d_pair(&p.a, bar, sa, kx, acol, ag);
-                }
-                if constexpr (B_MN) {
-                  tma_3d_pair(&p.b, bar, sb, brow, ky, bg);
-                  tma_3d_pair(&p.b, bar, sb + 8192, brow + 64, ky, bg);
-                } else if (half == 128) {
-                  tma_3d_pair(&p.b, bar, sb, kx, brow, bg);
-                } else {
-                  int r = 0;
-                  for (; r + 32 <= half; r += 32) tma_3d_pair(&p.b32, bar, sb + r * 128, kx, brow + r, bg);
-                  for (; r < half; r += 8) tma_3d_pair(&p.b8, bar, sb + r * 128, kx, brow + r, bg);
-                }
-              }
-            }
+          if (RAGGED == kRaggedK && ragged_tail(x.krows, kx)) {
+            // lands on this CTA's own barrier; warp 10 hands it on
+            mbar_arrive_expect_tx(&tail_bar[stage], bytes);
+            tma_3d(&p.a, &tail_bar[stage], sa, acol, ky, ag);
+            tma_3d(&p.a, &tail_bar[stage], sa + 8192, acol + 64, ky, ag);
+            tma_3d(bmap, &tail_bar[stage], sb, brow, ky, bg);
+            if (half > 64) tma_3d(bmap, &tail_bar[stage], sb + 8192, brow + 64, ky, bg);
+            continue;
+          }
+          const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+          if (leader) {
+            mbar_arrive_expect_tx(&full[stage], 2u * bytes);
+            if (RAGGED == kRaggedK) mbar_arrive(&full[stage]);
+          }
+          if (leader && p.withhold_first_load && it == 0) continue;
+          if constexpr (A_MN) {
+            tma_3d_pair(&p.a, bar, sa, acol, ky, ag);
+            tma_3d_pair(&p.a, bar, sa + 8192, acol + 64, ky, ag);
           } else {
-            // Both operands are MN-major: k row r of a box is the 128 bytes at r * 128 (the swizzle
-            // permutes within a row).  The block lands on this CTA's own barrier, its rows past the
-            // segment are zeroed in both operands (an infinity or NaN of the next segment must not
-            // meet a zero), and only then is the stage handed to the MMA.
-            const int valid = x.krows - kx;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(tail_bar, bytes);
-              tma_3d(&p.a, tail_bar, sa, acol, ky, ag);
-              tma_3d(&p.a, tail_bar, sa + 8192, acol + 64, ky, ag);
-              tma_3d(&p.b, tail_bar, sb, brow, ky, bg);
-              tma_3d(&p.b, tail_bar, sb + 8192, brow + 64, ky, bg);
-            }
-            bool landed = mbar_wait(tail_bar, tails & 1, kWaitLimitNs);
-            ++tails;
-            landed = __all_sync(0xffffffffu, landed);
-            if (!landed) {
-              ok = false;
-              break;
-            }
-            for (int o = valid * 128 + lane * 16; o < 8192; o += 512) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(sa + q * 8192 + o) = make_uint4(0, 0, 0, 0);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the tensor core reads them
-            __syncwarp();
-            if (lane == 0) {
-              if (leader) mbar_arrive(&full[stage]);
-              else mbar_arrive_cluster(mapa_shared(smem_u32(&full[stage]), 0));
-            }
+            tma_3d_pair(&p.a, bar, sa, kx, acol, ag);
+          }
+          if constexpr (B_MN) {
+            tma_3d_pair(bmap, bar, sb, brow, ky, bg);
+            if (half > 64) tma_3d_pair(bmap, bar, sb + 8192, brow + 64, ky, bg);
+          } else {
+            tma_3d_pair(bmap, bar, sb, kx, brow, bg);
           }
         }
       }
-      if (!ok && lane == 0) set_error(p.err, kErrTimeout);
+      if (!ok) set_error(p.err, kErrTimeout);
       // every stage this CTA filled must be consumed (the even CTA: landed) before shared memory is
       // released; after one expired wait the copies still in flight have long landed
-      if (lane == 0) {
-        const uint32_t issued = it;
-        for (int s = 0; s < kStages; ++s) {
-          if ((uint32_t)s >= issued) break;
-          const uint32_t last = issued - 1 - ((issued - 1 - s) % kStages);
-          const bool done = leader ? mbar_wait(&full[s], (last / kStages) & 1, kWaitLimitNs)
-                                   : mbar_wait(&empty[s], (last / kStages) & 1, kWaitLimitNs);
-          if (!done) {
-            set_error(p.err, kErrTimeout);
-            break;
-          }
+      for (int s = 0; s < kStages; ++s) {
+        if ((uint32_t)s >= it) break;
+        const uint32_t last = it - 1 - ((it - 1 - s) % kStages);
+        if (!mbar_wait(leader ? &full[s] : &empty[s], (last / kStages) & 1, kWaitLimitNs)) {
+          set_error(p.err, kErrTimeout);
+          break;
         }
       }
     }
@@ -542,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       bool ok = true;
       for (int i = cluster_id; i < sc.items && ok; i += n_clusters) {
         const Item x = item_of<RAGGED, EPI>(p, tile_start, sc, i);
-        const uint32_t idesc = p.idesc | ((uint32_t)(2 * half_of<B_MN>(x.nr)) >> 3 << 17) | (16u << 24);
+        const uint32_t idesc = p.idesc | ((uint32_t)(2 * half_of(x.nr)) >> 3 << 17) | (16u << 24);
         int kb = x.kb0;
         do {  // one use of an accumulator: the whole item, or one drain's K blocks; at least one
           const uint32_t buf = use & 1;
@@ -556,8 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           uint32_t accumulate = 0;
           for (; kb < end; ++kb, ++it) {
             const int stage = it % kStages;
-            const bool landed = RAGGED == kRaggedK ? mbar_wait_cluster(&full[stage], (it / kStages) & 1, kWaitLimitNs)
-                                                   : mbar_wait(&full[stage], (it / kStages) & 1, kWaitLimitNs);
+            // acquiring from the other CTA's threads costs about 800 cycles: only where they wrote
+            const bool landed = RAGGED == kRaggedK && ragged_tail(x.krows, kb * kBK)
+                                    ? mbar_wait_cluster(&full[stage], (it / kStages) & 1, kWaitLimitNs)
+                                    : mbar_wait(&full[stage], (it / kStages) & 1, kWaitLimitNs);
             if (!landed) {
               ok = false;
               break;
@@ -566,6 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kTileA;
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk) {
+              if (RAGGED == kRaggedK && kb * kBK + kk * 16 >= x.krows) break;  // behind the segment
               const uint64_t ad = A_MN ? mn_desc(sa + kk * 2048) : sw128_kmajor_desc(sa + kk * 32);
               const uint64_t bd = B_MN ? mn_desc(sb + kk * 2048) : sw128_kmajor_desc(sb + kk * 32);
               umma_bf16_pair(d, ad, bd, idesc, accumulate);
@@ -584,19 +663,56 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         if (!mbar_wait(&empty[last % kStages], (last / kStages) & 1, kWaitLimitNs)) set_error(p.err, kErrTimeout);
       }
     }
+  } else if (warp == 2 + kEpiWarps) {
+    // ------------------------------------------------------------------ tail blocks (kRaggedK, both CTAs)
+    // The rows of a segment's last block past its end belong to the next segment, and an infinity or
+    // NaN of theirs must not meet a zero.  Both operands are MN-major: k row r of a box is the 128 bytes
+    // at r * 128 (the swizzle permutes within a row), so once the block has landed its rows up to the
+    // next multiple of 16 are zeroed in both operands and the stage is handed to the MMA; the producer
+    // has gone on meanwhile.  Of the full barrier's two arrivals each CTA makes one here; for the other
+    // blocks the even CTA's producer makes both, so that no arrival crosses the pair.
+    if constexpr (RAGGED == kRaggedK) {
+      uint32_t it = 0, phases = 0;
+      bool ok = true;
+      for (int i = cluster_id; i < sc.items && ok; i += n_clusters) {
+        const Item x = item_of<RAGGED, EPI>(p, tile_start, sc, i);
+        const int count = x.kb1 - x.kb0, kx = (x.kb1 - 1) * kBK;
+        it += count;
+        if (count <= 0 || !ragged_tail(x.krows, kx)) continue;
+        const int stage = (it - 1) % kStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(&tail_bar[stage], (phases >> stage) & 1, kWaitLimitNs));
+        phases ^= 1u << stage;
+        if (!ok) break;
+        uint8_t* sa = smem + stage * kStageBytes;
+        const int valid = x.krows - kx, end = (valid + 15) / 16 * 16;
+        for (int o = valid * 128 + lane * 16; o < end * 128; o += 512) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(sa + q * 8192 + o) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(&full[stage]);
+          else mbar_arrive_cluster(mapa_shared(smem_u32(&full[stage]), 0));
+        }
+      }
+      if (!ok && lane == 0) set_error(p.err, kErrTimeout);
+    }
   } else {
     // ------------------------------------------------------------------ epilogue (warps 2..9, both CTAs)
     const int q = warp & 3;         // TMEM lane quarter this warp may read
     const int h = (warp - 2) >> 2;  // which 128 of the tile's rows
     uint32_t use = 0;
     bool ok = true;
+    Staging st = {staging + (warp - 2) * 4 * kChunkBytes, staging_bar + 2 * (warp - 2), 0};
     for (int i = cluster_id; i < sc.items && ok; i += n_clusters) {
       const Item x = item_of<RAGGED, EPI>(p, tile_start, sc, i);
       const int col = x.ct * kTile + (int)rank * 128 + q * 32 + lane;
       const bool none = x.kb1 <= x.kb0;
       const bool split = x.slot >= 0;
       float* mine = split ? part_ptr(p, x.slot, sc.split, x.part, (int)rank) + q * 32 + lane : nullptr;
-      const int chunks = max(0, min(4, (x.nr - h * 128 + 31) / 32));  // chunks of 32 rows with valid rows
+      // chunks of 32 rows with valid rows; none of a staged epilogue where no column is valid
+      const int chunks = kStaged && col - lane >= p.ld ? 0 : max(0, min(4, (x.nr - h * 128 + 31) / 32));
       if constexpr (kPromote) {
         float acc[4][32];
 #pragma unroll
@@ -614,11 +730,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               if (c < chunks) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(tacc + c * 32, r);
-                tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) acc[c][j] += __uint_as_float(r[j]);
+                for (int u = 0; u < 2; ++u) {  // 16 at a time: 128 sums and 16 addends fit the registers
+                  uint32_t r[16];
+                  tmem_ld_32x32b_x16(tacc + c * 32 + u * 16, r);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) acc[c][u * 16 + j] += __uint_as_float(r[j]);
+                }
               }
             }
           }
@@ -648,6 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
       } else {
         const uint32_t buf = use & 1;
+        if constexpr (kStaged)
+          if (!split && chunks > 0) fetch<EPI>(p, st, x.g, x.r0 + h * 128, col - lane, lane);
         ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (use >> 1) & 1, kWaitLimitNs));
         if (!ok) {
           if (lane == 0) set_error(p.err, kErrTimeout);
@@ -670,17 +791,29 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.0f;
           }
+          if (c == chunks - 1) {  // the accumulator has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+          }
           if (!split) {
-            emit<RAGGED, EPI>(p, x, v, j0, nj, col);
+            if constexpr (kStaged) {
+              const bool more = c + 1 < chunks;
+              if (more) fetch<EPI>(p, st, x.g, x.r0 + j0 + 32, col - lane, lane);
+              ok = emit_staged<EPI>(p, x, st, more ? 1 : 0, v, j0, nj, col, lane) && ok;
+            } else {
+              emit<RAGGED, EPI>(p, x, v, j0, nj, col);
+            }
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (j < nj) __stcg(mine + (size_t)(j0 + j) * 128, v[j]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+        if (chunks == 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+        }
         ++use;
       }
       if (split) {
@@ -698,20 +831,21 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           for (int c = 0; c < chunks; ++c) {
             const int j0 = h * 128 + c * 32;
             const int nj = min(32, x.nr - j0);
+            if constexpr (kStaged) fetch<EPI>(p, st, x.g, x.r0 + j0, col - lane, lane);
+            const float* first = part_ptr(p, x.slot, sc.split, 0, (int)rank) + (size_t)j0 * 128 + q * 32 + lane;
+            const size_t pitch = 2 * (size_t)p.prows * 128;
             float v[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-#pragma unroll 1
-            for (int s = 0; s < sc.split; ++s) {
-              const float* src = part_ptr(p, x.slot, sc.split, s, (int)rank) + (size_t)j0 * 128 + q * 32 + lane;
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (j < nj) v[j] += __ldcg(src + (size_t)j * 128);
-            }
-            emit<RAGGED, EPI>(p, x, v, j0, nj, col);
+            if (nj <= 4) add_parts<4, 16>(first, pitch, sc.split, nj, v);
+            else add_parts<16, 4>(first, pitch, sc.split, nj, v);
+            if constexpr (kStaged) ok = emit_staged<EPI>(p, x, st, 0, v, j0, nj, col, lane) && ok;
+            else emit<RAGGED, EPI>(p, x, v, j0, nj, col);
           }
         }
       }
+    }
+    if constexpr (kStaged) {
+      if (!ok && lane == 0) set_error(p.err, kErrTimeout);
+      if (lane == 0) bulk_wait();
     }
   }
 
@@ -745,18 +879,20 @@ inline EncodeFn encode_fn() {
   return fn;
 }
 
-// 16-bit row-major [groups, rows, inner] tensor, box of 64 elements x box_rows rows of one group,
-// 128-byte swizzle; what lies past inner or rows reads as zero.  inner is a multiple of 8.
+// 16-bit row-major [groups, rows, inner] tensor, box of box_inner elements x box_rows rows of one group,
+// 128-byte swizzle for an operand (64 elements), none for a staged chunk (32); what lies past inner or
+// rows reads as zero and is not written.  inner is a multiple of 8.
 inline bool make_map(CUtensorMap* m, bool bf16, const void* base, uint64_t inner, uint64_t rows, uint64_t groups,
-                     uint32_t box_rows) {
+                     uint32_t box_rows, uint32_t box_inner = 64) {
   EncodeFn enc = encode_fn();
   if (enc == nullptr || inner == 0 || rows == 0 || groups == 0) return false;
   cuuint64_t dims[3] = {inner, rows, groups};
   cuuint64_t strides[2] = {inner * 2, inner * rows * 2};
-  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t box[3] = {box_inner, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base),
-             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_inner == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -788,11 +924,14 @@ bool set_operands(Params& p, const OperandHost& a, const OperandHost& b, bool bf
   const uint32_t ty = bf16 ? 1u : 0u;
   p.idesc = (1u << 4) | (ty << 7) | (ty << 10) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16);
   if (!make_map(&p.a, bf16, a.base, a.inner, a.rows, a.groups, A_MN ? 64 : 128)) return false;
-  if (!make_map(&p.b, bf16, b.base, b.inner, b.rows, b.groups, B_MN ? 64 : 128)) return false;
-  if (!B_MN && (!make_map(&p.b32, bf16, b.base, b.inner, b.rows, b.groups, 32) ||
-                !make_map(&p.b8, bf16, b.base, b.inner, b.rows, b.groups, 8)))
-    return false;
+  for (int i = 0; i < (B_MN ? 1 : kBoxes); ++i)
+    if (!make_map(&p.b[i], bf16, b.base, b.inner, b.rows, b.groups, B_MN ? 64 : box_rows(i))) return false;
   return true;
+}
+
+// a staged epilogue's map of a 16-bit [groups, rows, inner] tensor
+inline bool set_chunks(CUtensorMap* m, const OperandHost& t) {
+  return make_map(m, false, t.base, t.inner, t.rows, t.groups, 32, 32);
 }
 
 template <bool A_MN, bool B_MN, int RAGGED, int EPI>
@@ -804,7 +943,7 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = smem_bytes(EPI);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -816,7 +955,7 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   cfg.attrs = attr;
   int clusters = dev >= 0 && dev < 64 ? cached[dev].load() : 0;
   if (clusters == 0) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(EPI));
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(2);
     cfg.numAttrs = 1;
