@@ -9,6 +9,7 @@ missing or the device is not a B200, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -299,15 +300,30 @@ def moe_combine(out_perm, inv_perm, shared_out, T, k, y=None, stream=None):
 
 
 # ------------------------------------------------------------------------------ grouped products
+# These entry points take some microseconds on the GPU at small sizes, so their checks are kept short.
+_DTYPE_CODES = {}
+
+
 def _dtype_code(dtype):
-    import torch
+    if not _DTYPE_CODES:
+        import torch
 
-    return {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16, torch.float32: MOE_DTYPE_FP32}[dtype]
+        _DTYPE_CODES.update({torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16,
+                             torch.float32: MOE_DTYPE_FP32})
+    return _DTYPE_CODES.get(dtype)
 
 
-def _need_on(t, device, name):
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+def _need_at(t, dtype, shape, index, name):
+    """a contiguous tensor of this type and shape on CUDA device ``index``"""
+    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+        return
+    _need(t, dtype, shape, name)
+    raise ValueError(f"{name}: expected a tensor on cuda:{index}, got {t.device}")
+
+
+@functools.lru_cache(maxsize=4096)
+def _ws_size(name, *sizes):
+    return getattr(lib(), name)(*sizes)
 
 
 def _product_ws(ws, need, device):
@@ -316,44 +332,52 @@ def _product_ws(ws, need, device):
 
     if ws is None or ws.numel() < need:
         return torch.zeros(need, dtype=torch.uint8, device=device)
-    _need(ws, torch.uint8, None, "ws")
-    _need_on(ws, device, "ws")
+    if not (ws.dtype is torch.uint8 and ws.is_cuda and ws.is_contiguous() and ws.device == device):
+        raise ValueError(f"ws: expected a contiguous uint8 tensor on {device}")
     return ws
 
 
-def _on_device(device, stream):
-    """(a context that makes ``device`` current, the handle of ``stream`` or of its current stream)."""
+def _launch(name, device, stream, *args):
+    """Calls the C entry point with ``args`` and the stream on ``device``."""
     import torch
 
-    return torch.cuda.device(device), (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = getattr(lib(), name)(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = getattr(lib(), name)(*args, handle)
+    if status != 0:
+        raise MoeError(status, name)
 
 
 def _rows_product(name, rows, offsets, w, contracted, wide, out, out_dtype, ws, stream):
     import torch
 
-    if rows.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"expected bfloat16 or float16 rows, got {rows.dtype}")
+    dtype = rows.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"expected bfloat16 or float16 rows, got {dtype}")
     if rows.dim() != 2 or w.dim() != 3:
         raise ValueError("expected rows [M, .] and w [E, N, K]")
-    E, N, K = w.shape
+    sizes = w.shape
+    E, N, K = sizes
     M = rows.shape[0]
-    _need(rows, rows.dtype, (M, w.shape[contracted]), "x" if contracted == 2 else "dy")
-    _need(w, rows.dtype, None, "w")
-    _need(offsets, torch.int32, (E + 1,), "offsets")
-    out_dtype = out_dtype or (rows.dtype if out is None else out.dtype)
-    if out_dtype not in (rows.dtype, torch.float32):
-        raise ValueError(f"out_dtype: expected {rows.dtype} or torch.float32, got {out_dtype}")
+    index = rows.get_device()
+    _need_at(rows, dtype, (M, sizes[contracted]), index, "x" if contracted == 2 else "dy")
+    _need_at(w, dtype, sizes, index, "w")
+    _need_at(offsets, torch.int32, (E + 1,), index, "offsets")
+    if out_dtype is None:
+        out_dtype = dtype if out is None else out.dtype
+    if out_dtype is not dtype and out_dtype is not torch.float32:
+        raise ValueError(f"out_dtype: expected {dtype} or torch.float32, got {out_dtype}")
+    device = rows.device
     if out is None:
-        out = torch.empty(M, w.shape[wide], dtype=out_dtype, device=rows.device)
-    _need(out, out_dtype, (M, w.shape[wide]), "out")
-    for t, n in ((w, "w"), (offsets, "offsets"), (out, "out")):
-        _need_on(t, rows.device, n)
-    ws = _product_ws(ws, lib().moe_grouped_gemm_workspace_size(M), rows.device)
-    device, handle = _on_device(rows.device, stream)
-    with device:
-        _check(getattr(lib(), name)(rows.data_ptr(), offsets.data_ptr(), w.data_ptr(), M, E, N, K,
-                                    _dtype_code(rows.dtype), _dtype_code(out_dtype), out.data_ptr(), ws.data_ptr(),
-                                    ws.numel(), handle), name)
+        out = torch.empty(M, sizes[wide], dtype=out_dtype, device=device)
+    else:
+        _need_at(out, out_dtype, (M, sizes[wide]), index, "out")
+    ws = _product_ws(ws, _ws_size("moe_grouped_gemm_workspace_size", M), device)
+    _launch(name, device, stream, rows.data_ptr(), offsets.data_ptr(), w.data_ptr(), M, E, N, K, _dtype_code(dtype),
+            _dtype_code(out_dtype), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out, ws
 
 
@@ -375,26 +399,25 @@ def moe_grouped_gemm_wgrad(dy, x, offsets, out=None, ws=None, stream=None):
     dy [M, N], x [M, K] -> (dw [E, N, K] fp32, ws); zeros for an expert without rows."""
     import torch
 
-    if dy.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"expected bfloat16 or float16 rows, got {dy.dtype}")
+    dtype = dy.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"expected bfloat16 or float16 rows, got {dtype}")
     if dy.dim() != 2 or x.dim() != 2 or offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError("expected dy [M, N], x [M, K] and offsets [E+1]")
     M, N = dy.shape
     K, E = x.shape[1], offsets.numel() - 1
-    _need(dy, dy.dtype, None, "dy")
-    _need(x, dy.dtype, (M, K), "x")
-    _need(offsets, torch.int32, None, "offsets")
+    index = dy.get_device()
+    _need_at(dy, dtype, (M, N), index, "dy")
+    _need_at(x, dtype, (M, K), index, "x")
+    _need_at(offsets, torch.int32, (E + 1,), index, "offsets")
+    device = dy.device
     if out is None:
-        out = torch.empty(E, N, K, dtype=torch.float32, device=dy.device)
-    _need(out, torch.float32, (E, N, K), "out")
-    for t, n in ((x, "x"), (offsets, "offsets"), (out, "out")):
-        _need_on(t, dy.device, n)
-    ws = _product_ws(ws, lib().moe_grouped_gemm_wgrad_workspace_size(N), dy.device)
-    device, handle = _on_device(dy.device, stream)
-    with device:
-        _check(lib().moe_grouped_gemm_wgrad(dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), M, E, N, K,
-                                            _dtype_code(dy.dtype), out.data_ptr(), ws.data_ptr(), ws.numel(), handle),
-               "moe_grouped_gemm_wgrad")
+        out = torch.empty(E, N, K, dtype=torch.float32, device=device)
+    else:
+        _need_at(out, torch.float32, (E, N, K), index, "out")
+    ws = _product_ws(ws, _ws_size("moe_grouped_gemm_wgrad_workspace_size", N), device)
+    _launch("moe_grouped_gemm_wgrad", device, stream, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), M, E, N, K,
+            _dtype_code(dtype), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out, ws
 
 
@@ -405,27 +428,27 @@ def moe_orthogonalize(g, steps=5, out=None, ws=None, stream=None):
     dgate_up.view(2 * E, F, D) and ddown."""
     import torch
 
-    if g.dtype not in (torch.float32, torch.bfloat16):
+    if g.dtype is not torch.float32 and g.dtype is not torch.bfloat16:
         raise ValueError(f"g: expected float32 or bfloat16, got {g.dtype}")
     if g.dim() < 2:
         raise ValueError("g: expected [..., M, N]")
-    _need(g, g.dtype, None, "g")
+    index = g.get_device()
+    _need_at(g, g.dtype, g.shape, index, "g")
+    device = g.device
     M, N = g.shape[-2:]
     if out is None:
-        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
-    _need(out, torch.bfloat16, tuple(g.shape), "out")
-    _need_on(out, g.device, "out")
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=device)
+    else:
+        _need_at(out, torch.bfloat16, g.shape, index, "out")
     B = g.numel() // (M * N) if M * N else 0
     if B == 0:
         return out, ws
-    need = lib().moe_orthogonalize_workspace_size(B, M, N)
+    need = _ws_size("moe_orthogonalize_workspace_size", B, M, N)
     if need == 0:
         raise MoeError(2, "moe_orthogonalize_workspace_size")
-    ws = _product_ws(ws, need, g.device)
-    device, handle = _on_device(g.device, stream)
-    with device:
-        _check(lib().moe_orthogonalize(g.data_ptr(), _dtype_code(g.dtype), B, M, N, int(steps), out.data_ptr(),
-                                       ws.data_ptr(), ws.numel(), handle), "moe_orthogonalize")
+    ws = _product_ws(ws, need, device)
+    _launch("moe_orthogonalize", device, stream, g.data_ptr(), _dtype_code(g.dtype), B, M, N, int(steps),
+            out.data_ptr(), ws.data_ptr(), ws.numel())
     return out, ws
 
 

@@ -111,12 +111,15 @@ moe_status_t moe_grouped_gemm_wgrad(const void* dy, const void* x, const int32_t
   p.kb_typ = (M / E + kBK - 1) / kBK;  // the mean segment
   p.rows_typ = N;
   p.out = dw;
+  p.ld = K;
+  const OperandHost out = {dw, (uint64_t)K, (uint64_t)N, (uint64_t)E};
+  if (!set_chunks(&p.out_map, out, true) || !set_chunks(&p.out_lo_map, out, true, 16)) return MOE_ERR_CUDA;
   p.withhold_first_load = test_withhold_this_launch() ? 1 : 0;
   set_workspace(p, ws, partial_rows(N));
   const OperandHost a = {x, (uint64_t)K, (uint64_t)M, 1};
   const OperandHost b = {dy, (uint64_t)N, (uint64_t)M, 1};
   if (!set_operands<true, true>(p, a, b, dtype == MOE_DTYPE_BF16)) return MOE_ERR_CUDA;
-  return launch_status(launch<true, true, kRaggedK, kOut32>(p, s));
+  return launch_status(launch<true, true, kRaggedK, kGrad>(p, s));
 }
 
 }  // extern "C"

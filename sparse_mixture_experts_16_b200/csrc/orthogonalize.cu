@@ -151,7 +151,7 @@ struct Layout {
 };
 
 // Enough matrices side by side that the launch with the fewest tiles, the Gram matrix's, fills four rounds
-// of 74 clusters, within 1 GB of X; dealt evenly over the rounds of launches.
+// of 74 clusters, within 1 GB of X.
 constexpr long long kTargetTiles = 296;
 constexpr long long kBatchBytes = 1LL << 30;
 
@@ -164,8 +164,7 @@ bool layout_of(int B, int M, int N, Layout& l) {
   long long batch = (kTargetTiles + tiles - 1) / tiles;
   const long long fits = kBatchBytes / (6LL * M * l.np);
   if (batch > fits) batch = fits > 1 ? fits : 1;
-  const long long rounds = (B + batch - 1) / batch;
-  l.batch = (int)((B + rounds - 1) / rounds);
+  l.batch = B < batch ? B : (int)batch;
   l.prows = partial_rows(M);
   size_t at = align_up(kPartialOffset + partial_bytes(l.prows), 256);
   auto take = [&](size_t bytes) {
@@ -308,8 +307,9 @@ moe_status_t moe_orthogonalize(const void* g, int g_dtype, int B, int M, int N, 
   if (st != MOE_OK) return st;
   uint8_t* b = static_cast<uint8_t*>(ws);
   cudaStream_t s = (cudaStream_t)stream;
-  for (int at = 0; at < B; at += l.batch) {
-    const int count = B - at < l.batch ? B - at : l.batch;
+  const int rounds = (B + l.batch - 1) / l.batch, most = (B + rounds - 1) / rounds;  // dealt evenly
+  for (int at = 0; at < B; at += most) {
+    const int count = B - at < most ? B - at : most;
     const long long skip = (long long)at * M * N;
     cudaError_t e = g_dtype == MOE_DTYPE_FP32
                         ? prepare(static_cast<const float*>(g) + skip, count, M, N, l, b, s)

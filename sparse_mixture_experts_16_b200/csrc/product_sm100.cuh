@@ -57,7 +57,8 @@ enum Epilogue {
   kGram = 2,      // symmetric: out = fp16(acc * c1), and its mirror image
   kPoly = 3,      // symmetric: out = fp16(c0 * src + acc * c1), and its mirror image
   kApply = 4,     // x = c0 * (src + src_lo / 2048) + acc * c1; out = fp16(x), out_lo = fp16(2048 (x - out))
-  kApplyLast = 5  // out = bf16(the same x * c2), rows of ld_out elements
+  kApplyLast = 5, // out = bf16(the same x * c2), rows of cols_out elements
+  kGrad = 6       // as kOut32, of groups of equal rows: leaves by TMA
 };
 
 constexpr int kTile = 256;               // rows (N) and columns (M) of a pair's tile
@@ -72,13 +73,18 @@ constexpr int kPromoteBlocks = 8;        // K blocks per accumulator drain (512 
 constexpr int kMaxGroups = 1024;
 constexpr int kBarBytes = 384;  // 3 per stage, 4 of the accumulators, 16 of the staging, the tensor memory's address
 constexpr int kChunkBytes = 32 * 32 * 2;  // 32 rows x 32 columns of 16 bits: what a warp's epilogue handles at a time
-constexpr int kStagingBytes = kEpiWarps * 2 * 2 * kChunkBytes;  // two buffers of two arrays per warp
-constexpr bool staged(int epi) { return epi == kPoly || epi == kApply || epi == kApplyLast; }
-constexpr int stages_of(int epi) { return staged(epi) ? kStages - 1 : kStages; }
+constexpr bool staged(int epi) { return epi == kPoly || epi == kApply || epi == kApplyLast; }  // adds to 16-bit tiles
+constexpr bool by_tma(int epi) { return staged(epi) || epi == kGrad; }  // loads or stores by TMA
+// staging per epilogue warp: two buffers of two 16-bit arrays or of fp32 by TMA; one for a 16-bit transposition
+constexpr int staging_of(int epi) { return by_tma(epi) ? 4 * kChunkBytes : epi == kOut16 || epi == kGram ? kChunkBytes : 0; }
+constexpr int stages_of(int epi) { return by_tma(epi) ? kStages - 1 : kStages; }
+// groups whose segments' bounds are held in shared memory (kGrad: what the staging leaves room for)
+constexpr int table_groups(int epi) { return epi == kGrad ? 190 : kMaxGroups; }
 constexpr size_t smem_bytes(int epi) {
-  return 1024 + (size_t)stages_of(epi) * kStageBytes + kBarBytes + (staged(epi) ? kStagingBytes + 16 : 4 * (kMaxGroups + 4));
+  return 1024 + (size_t)stages_of(epi) * kStageBytes + kBarBytes + kEpiWarps * staging_of(epi) +
+         16 + 4 * (epi == kGrad ? 2 * table_groups(epi) : epi <= kOut32 ? 3 * kMaxGroups : 0);
 }
-static_assert(smem_bytes(kOut32) <= 232448 && smem_bytes(kApply) <= 232448, "shared memory budget");
+static_assert(smem_bytes(kOut16) <= 232448 && smem_bytes(kApply) <= 232448 && smem_bytes(kGrad) <= 232448, "shared memory budget");
 
 // workspace of a launch: error word, counters (zero between launches), split-K partial sums
 constexpr int kMaxParts = 148;           // split tiles x parts
@@ -99,7 +105,9 @@ struct alignas(64) Params {
   CUtensorMap a;          // K-major: box 64 k x 128 columns; MN-major: box 64 columns x 64 k
   CUtensorMap b[kBoxes];  // K-major: boxes of 64 k x box_rows(i) rows; MN-major (the first): 64 rows x 64 k
   const int32_t* offsets;  // kRaggedRows / kRaggedK: segment bounds [G + 1]
-  CUtensorMap src_map;     // staged epilogues: src, src_lo, out, out_lo in boxes of 32 columns x 32 rows
+  // boxes of 32 columns x 32 rows: src, src_lo, out and out_lo of the staged epilogues, out of kGrad, whose
+  // out_lo_map is out in boxes of 16 rows
+  CUtensorMap src_map;
   CUtensorMap src_lo_map;
   CUtensorMap out_map;
   CUtensorMap out_lo_map;
@@ -150,6 +158,12 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
       : "memory");
   return ok != 0;
 }
+// Arrive on an mbarrier of the pair's even CTA, ordering nothing beyond this CTA: the reads of tensor memory
+// that it reports have completed (tcgen05.wait::ld).  A release at cluster scope first waits for the
+// thread's global stores, 3500 cycles a tile here.
+__device__ __forceinline__ void mbar_arrive_even(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0)) : "memory");
+}
 // as mbar_wait, seeing what the other CTA wrote before its arrival
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   const uint32_t a = smem_u32(bar);
@@ -168,6 +182,7 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // generic accesses of shared memory before -> the TMA's or the tensor core's after
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -178,10 +193,17 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr) {
 }
 
 // ------------------------------------------------------------------------------ schedule
+constexpr int kBand = 8;  // row tiles of a band (item_of)
+
 struct Sched {
   int full;   // tiles dealt whole
   int split;  // parts of each later tile
   int items;
+  int lr;     // a tile has at most 2^lr rows
+  int ct;     // column tiles
+  int per;    // not kRaggedRows: tiles of a group, rows of a tile
+  int step;
+  float inv_split, inv_band, inv_per;
 };
 
 // Parts of each of the r < clusters tiles of the last round.  Cost in K blocks (of about 0.3 us): rounds
@@ -192,7 +214,7 @@ struct Sched {
 __device__ __forceinline__ int split_of(int r, int clusters, int kb, int rows) {
   if (r <= 0) return 1;
   const int most = min(kMaxSplit, min(kb / 2, kMaxParts / r));
-  const float groups = (float)((min(rows, 128) + 15) / 16);
+  const float groups = (float)((rows + 15) / 32);  // of 16 rows, per warp
   int best = 1;
   float cost = 1e30f;
   for (int s = 1; s <= most || s == 1; ++s) {
@@ -210,6 +232,7 @@ struct Item {
   int row0;          // kRaggedRows: first row of the segment
   int k0, krows;     // kRaggedK: first k row and number of k rows
   int kb0, kb1;      // K blocks [kb0, kb1)
+  bool triangle;     // a symmetric product's mirror image is stored too
   int part, slot;    // part of the split, split-tile index (-1: whole)
 };
 
@@ -221,46 +244,79 @@ __device__ __forceinline__ void segment(const Params& p, int g, int& row0, int& 
   bad = row0 != a || end != b;
 }
 
-template <int RAGGED, int EPI>
-__device__ __forceinline__ int tiles_of(const Params& p, int rows) {
-  const int rt = (rows + kTile - 1) / kTile;
-  if constexpr (EPI == kGram || EPI == kPoly) return rt * (rt + 1) / 2;
+// Tiles of a group of `rows` rows, at most 2^lr of them in a tile.  With fewer tiles than clusters the limit
+// is 128 or 64 rows, so that more of the machine takes part and the epilogues get shorter.  Of a symmetric
+// product only the lower triangle of 256 x 256 tiles is computed, but all of the smaller tiles.
+constexpr int kMostLr = 8, kLeastLr = 6;
+constexpr bool symmetric(int epi) { return epi == kGram || epi == kPoly; }
+template <int EPI>
+__device__ __forceinline__ int tiles_of(const Params& p, int rows, int lr) {
+  const int rt = (rows + (1 << lr) - 1) >> lr;
+  if (symmetric(EPI) && lr == kMostLr) return rt * (rt + 1) / 2;
   return rt * ((p.cols + kTile - 1) / kTile);
 }
 
+// n / d for quotients below 2^22, inv = 1 / d: the estimate is off by at most one (every role divides for every
+// tile, and a tile of few K blocks is worth only some thousand cycles)
+__device__ __forceinline__ int divide(int n, int d, float inv, int& rem) {
+  int q = (int)((float)n * inv);
+  rem = n - q * d;
+  if (rem < 0) --q, rem += d;
+  if (rem >= d) ++q, rem -= d;
+  return q;
+}
+
+// Rows of a tile of a group.  They are dealt evenly over its rt row tiles, in 16s: a tile of few rows costs
+// nearly half a full one, for the columns' operand comes in whole.  The symmetric products keep square
+// tiles, and what leaves in boxes of 32 rows tiles of whole boxes.
+template <int EPI>
+__device__ __forceinline__ int step_of(int rows, int rt, int lr) {
+  constexpr int kUnit = staged(EPI) ? 32 : 16;
+  if (symmetric(EPI) || rt == 1) return 1 << lr;
+  return ((rows + rt - 1) / rt + kUnit - 1) / kUnit * kUnit;
+}
+
+// tab: kRaggedRows, kRaggedK: first row and rows of each group; kRaggedRows: then the first tile of each
 template <int RAGGED, int EPI>
-__device__ __forceinline__ Item item_of(const Params& p, const int* tile_start, const Sched& sc, int i) {
+__device__ __forceinline__ Item item_of(const Params& p, const int* tab, const Sched& sc, int i) {
   Item x;
   int t = i;
   int parts = 1;
   x.part = 0;
   x.slot = -1;
   if (i >= sc.full && sc.split > 1) {
-    x.slot = (i - sc.full) / sc.split;
-    x.part = (i - sc.full) - x.slot * sc.split;
+    x.slot = divide(i - sc.full, sc.split, sc.inv_split, x.part);
     t = sc.full + x.slot;
     parts = sc.split;
   }
   int rows = p.rows, local;
   x.row0 = 0, x.k0 = 0, x.krows = 0;
-  bool bad;
   if constexpr (RAGGED == kRaggedRows) {
+    const int* tile_start = tab + 2 * p.G;
     int lo = 0, hi = p.G - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (tile_start[mid] <= t) lo = mid; else hi = mid - 1;
     }
     x.g = lo;
-    segment(p, lo, x.row0, rows, bad);
+    x.row0 = tab[2 * lo];
+    rows = tab[2 * lo + 1];
     local = t - tile_start[lo];
   } else {
-    const int per = tiles_of<RAGGED, EPI>(p, p.rows);
-    x.g = t / per;
-    local = t - x.g * per;
-    if constexpr (RAGGED == kRaggedK) segment(p, x.g, x.k0, x.krows, bad);
+    x.g = divide(t, sc.per, sc.inv_per, local);
+    if constexpr (RAGGED == kRaggedK) {
+      if (p.G <= table_groups(EPI)) {
+        x.k0 = tab[2 * x.g];
+        x.krows = tab[2 * x.g + 1];
+      } else {
+        bool bad;
+        segment(p, x.g, x.k0, x.krows, bad);
+      }
+    }
   }
-  const int rt = (rows + kTile - 1) / kTile;
-  if constexpr (EPI == kGram || EPI == kPoly) {
+  const int rt = (rows + (1 << sc.lr) - 1) >> sc.lr;
+  x.triangle = symmetric(EPI) && sc.lr == kMostLr;
+  if (x.triangle) {
     // lower triangle, row by row
     int r = (int)((sqrtf(8.0f * (float)local + 1.0f) - 1.0f) * 0.5f);
     while (r * (r + 1) / 2 > local) --r;
@@ -270,23 +326,21 @@ __device__ __forceinline__ Item item_of(const Params& p, const int* tile_start, 
   } else {
     // bands of 8 row tiles, rows fastest inside a band: the ~74 tiles in flight share about 8 row
     // blocks and 9 column blocks through L2
-    const int ct = (p.cols + kTile - 1) / kTile;
-    const int band = local / (8 * ct);
-    const int rem = local - band * 8 * ct;
-    const int rb = min(8, rt - 8 * band);
-    x.ct = rem / rb;
-    x.rt = 8 * band + (rem - x.ct * rb);
+    int rem, in_band;
+    const int band = divide(local, kBand * sc.ct, sc.inv_band, rem);
+    const int rb = min(kBand, rt - kBand * band);
+    x.ct = divide(rem, rb, __fdividef(1.0f, (float)rb), in_band);
+    x.rt = kBand * band + in_band;
   }
-  // Rows are dealt evenly over the tiles, in 16s: a tile of few rows costs nearly half a full one, for
-  // the columns' operand comes in whole.  The symmetric products keep square tiles, and what leaves in
-  // boxes of 32 rows tiles of whole boxes.
-  constexpr int kUnit = staged(EPI) ? 32 : 16;
-  const int step = EPI == kGram || EPI == kPoly ? kTile : ((rows + rt - 1) / rt + kUnit - 1) / kUnit * kUnit;
+  const int step = RAGGED == kRaggedRows ? step_of<EPI>(rows, rt, sc.lr) : sc.step;
   x.r0 = x.rt * step;
   x.nr = min(step, rows - x.r0);
   const int kb = RAGGED == kRaggedK ? (x.krows + kBK - 1) / kBK : (p.K + kBK - 1) / kBK;
-  x.kb0 = split_begin(kb, x.part, parts);
-  x.kb1 = split_end(kb, x.part, parts);
+  x.kb0 = 0, x.kb1 = kb;
+  if (parts > 1) {
+    x.kb0 = split_begin(kb, x.part, parts);
+    x.kb1 = split_end(kb, x.part, parts);
+  }
   return x;
 }
 
@@ -300,56 +354,81 @@ __device__ __forceinline__ bool ragged_tail(int krows, int kx) { return kx + kBK
 __device__ __forceinline__ uint16_t half_bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
 __device__ __forceinline__ float half_val(uint16_t b) { return __half2float(__ushort_as_half(b)); }
 
-// Symmetric products: h[j], the values of rows row_in + j and column col, as row col, columns row_in + j
-__device__ __forceinline__ void mirror(const Params& p, const Item& x, const uint16_t (&h)[32], int row_in, int col) {
-  if (x.rt == x.ct || col >= p.rows) return;
+// Symmetric products: the values of rows row_in + 2 i and + 1, column col, packed in w[i], as row col,
+// columns row_in ..
+__device__ __forceinline__ void mirror(const Params& p, const Item& x, const uint32_t (&w)[16], int row_in, int col) {
+  if (!x.triangle || x.rt == x.ct || col >= p.rows) return;
   uint16_t* m = static_cast<uint16_t*>(p.out) + ((long long)x.g * p.rows + col) * p.ld + row_in;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    if (row_in + 8 * u + 8 <= p.ld) {
-      uint4 w;
-      w.x = (uint32_t)h[8 * u] | (uint32_t)h[8 * u + 1] << 16;
-      w.y = (uint32_t)h[8 * u + 2] | (uint32_t)h[8 * u + 3] << 16;
-      w.z = (uint32_t)h[8 * u + 4] | (uint32_t)h[8 * u + 5] << 16;
-      w.w = (uint32_t)h[8 * u + 6] | (uint32_t)h[8 * u + 7] << 16;
-      *reinterpret_cast<uint4*>(m + 8 * u) = w;
-    }
-  }
+  for (int u = 0; u < 4; ++u)
+    if (row_in + 8 * u + 8 <= p.ld)
+      *reinterpret_cast<uint4*>(m + 8 * u) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // One warp's 32 rows x 32 columns, v[j] = accumulator of row j0 + j and column col (this lane's); nj rows
-// are valid.  A row of 32 columns is one store of a warp.
+// are valid.  16-bit results are packed by pairs of rows, turned through shared memory and stored 16 bytes
+// a lane: a store per element made this half of the epilogue's 6000 cycles a tile.  A row of 32 fp32 is one
+// store of a warp.
 template <int RAGGED, int EPI>
-__device__ __forceinline__ void emit(const Params& p, const Item& x, const float (&v)[32], int j0, int nj, int col) {
+__device__ __forceinline__ void emit(const Params& p, const Item& x, uint8_t* buf, const float (&v)[32], int j0, int nj,
+                                     int col, int lane) {
   const int row_in = x.r0 + j0;  // row within the group
   const long long row = (RAGGED == kRaggedRows ? (long long)x.row0 : (long long)x.g * p.rows) + row_in;
-  if constexpr (EPI == kOut16) {
-    if (col >= p.cols) return;
-    uint16_t* o = static_cast<uint16_t*>(p.out) + row * p.cols + col;
-    const bool bf = p.out_bf16 != 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (j < nj) {
-        const uint16_t h = bf ? __bfloat16_as_ushort(__float2bfloat16_rn(v[j])) : half_bits(v[j]);
-        o[(long long)j * p.cols] = h;
-      }
-    }
-  } else if constexpr (EPI == kOut32) {
+  if constexpr (EPI == kOut32) {
     if (col >= p.cols) return;
     float* o = static_cast<float*>(p.out) + row * p.cols + col;
+    if (nj == 32) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < nj) o[(long long)j * p.cols] = v[j];
-  } else {  // kGram
-    uint16_t h[32];
-    uint16_t* o = static_cast<uint16_t*>(p.out) + row * p.ld + col;
-    const bool col_ok = col < p.ld;
+      for (int j = 0; j < 32; ++j) o[(long long)j * p.cols] = v[j];
+    } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      h[j] = half_bits(v[j] * p.c1);
-      if (col_ok && j < nj) o[(long long)j * p.ld] = h[j];
+      for (int j = 0; j < 32; ++j)
+        if (j < nj) o[(long long)j * p.cols] = v[j];
     }
-    mirror(p, x, h, row_in, col);
+  } else {  // kOut16, kGram
+    uint32_t w[16];
+    if (EPI == kOut16 && p.out_bf16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    } else {
+      const float c = EPI == kGram ? p.c1 : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = pack_half(v[2 * i] * c, v[2 * i + 1] * c);
+    }
+    uint32_t* b = reinterpret_cast<uint32_t*>(buf);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) b[i * 32 + lane] = w[i];
+    __syncwarp();
+    const int pitch = EPI == kGram ? p.ld : p.cols;
+    const int c8 = (lane & 3) * 8;  // eight columns of a pair of rows
+    uint16_t* o = static_cast<uint16_t*>(p.out) + row * pitch + (col - lane + c8);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int pair = (lane >> 2) + 8 * i;
+      const uint4 l = *reinterpret_cast<const uint4*>(b + pair * 32 + c8);
+      const uint4 h = *reinterpret_cast<const uint4*>(b + pair * 32 + c8 + 4);
+      if (col - lane + c8 < pitch) {
+        if (2 * pair < nj)
+          *reinterpret_cast<uint4*>(o + (long long)(2 * pair) * pitch) =
+              make_uint4(__byte_perm(l.x, l.y, 0x5410), __byte_perm(l.z, l.w, 0x5410), __byte_perm(h.x, h.y, 0x5410),
+                         __byte_perm(h.z, h.w, 0x5410));
+        if (2 * pair + 1 < nj)
+          *reinterpret_cast<uint4*>(o + (long long)(2 * pair + 1) * pitch) =
+              make_uint4(__byte_perm(l.x, l.y, 0x7632), __byte_perm(l.z, l.w, 0x7632), __byte_perm(h.x, h.y, 0x7632),
+                         __byte_perm(h.z, h.w, 0x7632));
+      }
+    }
+    __syncwarp();  // the buffer is written again
+    if constexpr (EPI == kGram) mirror(p, x, w, row_in, col);
   }
 }
 
@@ -387,13 +466,14 @@ __device__ __forceinline__ bool emit_staged(const Params& p, const Item& x, cons
   if (!__all_sync(0xffffffffu, mbar_wait(&st.bar[n & 1], (n >> 1) & 1, kWaitLimitNs))) return false;
   const int row = x.r0 + j0, col0 = col - lane;
   if constexpr (EPI == kPoly) {
-    uint16_t h[32];
+    uint32_t w[16];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      h[j] = half_bits(v[j] * p.c1 + p.c0 * half_val(hi[j * 32]));
-      hi[j * 32] = h[j];
+    for (int i = 0; i < 16; ++i) {
+      w[i] = pack_half(v[2 * i] * p.c1 + p.c0 * half_val(hi[i * 64]), v[2 * i + 1] * p.c1 + p.c0 * half_val(hi[i * 64 + 32]));
+      hi[i * 64] = (uint16_t)w[i];
+      hi[i * 64 + 32] = (uint16_t)(w[i] >> 16);
     }
-    mirror(p, x, h, row, col);
+    mirror(p, x, w, row, col);
   } else {
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
@@ -421,6 +501,23 @@ __device__ __forceinline__ bool emit_staged(const Params& p, const Item& x, cons
     bulk_commit();
   }
   return true;
+}
+
+// kGrad: rows j0 + [0, nj) leave as one box of 32 x 32 (16 x 32 at the end of a tile) from the buffer
+// whose last store was the last but one; what lies past the matrix is not written
+__device__ __forceinline__ void emit_grad(const Params& p, const Item& x, Staging& st, const float (&v)[32], int j0,
+                                          int nj, int col, int lane) {
+  float* b = reinterpret_cast<float*>(st.buf + (st.n++ & 1) * 2 * kChunkBytes);
+  if (lane == 0) bulk_wait_read_but_one();
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 32; ++j) b[j * 32 + lane] = v[j];
+  fence_async();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(nj > 16 ? &p.out_map : &p.out_lo_map, b, col - lane, x.r0 + j0, x.g);
+    bulk_commit();
+  }
 }
 
 // the sum of a split tile's parts over rows j0 + [0, 32), in the order of the parts, ROWS x PARTS loads in
@@ -456,7 +553,7 @@ __device__ __forceinline__ float* part_ptr(const Params& p, int slot, int split,
 // ------------------------------------------------------------------------------ the kernel
 template <bool A_MN, bool B_MN, int RAGGED, int EPI>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p) {
-  constexpr bool kPromote = EPI == kOut32, kStaged = staged(EPI);
+  constexpr bool kPromote = EPI == kOut32 || EPI == kGrad, kStaged = staged(EPI);
   constexpr int kStages = stages_of(EPI);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -468,9 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   uint64_t* staging_bar = tail_bar + kStages;                                 // staged: two per epilogue warp
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(staging_bar + 2 * kEpiWarps);
   uint8_t* staging = smem + kStages * kStageBytes + kBarBytes;
-  int* sched_smem = reinterpret_cast<int*>(staging + (kStaged ? kStagingBytes : 0));
-  int* tile_start = sched_smem + 3;  // kRaggedRows: [G + 1]
+  int* sched_smem = reinterpret_cast<int*>(staging + kEpiWarps * staging_of(EPI));
+  int* tab = sched_smem + 4;  // item_of's table
 
+  // the parameters' lines are fetched while the barriers are set up, not one by one where they are used
+  asm volatile("" ::"r"(p.G), "r"(p.rows), "r"(p.cols), "r"(p.K), "r"(p.ld), "r"(p.prows), "r"(p.kb_typ), "l"(p.err));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -503,39 +602,53 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       bool bad;
       segment(p, g, row0, rows, bad);
       if (bad && blockIdx.x == 0) set_error(p.err, kErrBadIndex);
-      if constexpr (RAGGED == kRaggedRows) tile_start[g] = tiles_of<RAGGED, EPI>(p, rows);
+      if (p.G <= table_groups(EPI)) {
+        tab[2 * g] = row0;
+        tab[2 * g + 1] = rows;
+      }
     }
   }
   __syncthreads();
   if (warp == 0) {
-    int total;
-    if constexpr (RAGGED == kRaggedRows) {  // exclusive scan of the groups' tile counts
-      const int per = (p.G + 31) / 32;
-      const int lo = min(p.G, lane * per), hi = min(p.G, lo + per);
-      int sum = 0;
-      for (int g = lo; g < hi; ++g) sum += tile_start[g];
-      int incl = sum;
+    int total[3] = {0, 0, 0};  // tiles of at most 64, 128, 256 rows
+    const int per = (p.G + 31) / 32;  // kRaggedRows: groups of a lane
+    const int lo = min(p.G, lane * per), hi = min(p.G, lo + per);
+    if constexpr (RAGGED == kRaggedRows) {
+      for (int g = lo; g < hi; ++g)
+#pragma unroll
+        for (int u = 0; u < 3; ++u) total[u] += tiles_of<EPI>(p, tab[2 * g + 1], kLeastLr + u);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 3; ++u) total[u] = p.G * tiles_of<EPI>(p, p.rows, kLeastLr + u);
+    }
+    int sum[3] = {total[0], total[1], total[2]};
+    if constexpr (RAGGED == kRaggedRows) {
+#pragma unroll
+      for (int u = 0; u < 3; ++u) total[u] = __reduce_add_sync(0xffffffffu, total[u]);
+    }
+    const int size = total[2] > n_clusters || total[1] > n_clusters ? 2 : total[0] > n_clusters ? 1 : 0;
+    const int lr = kLeastLr + size, all = size == 2 ? total[2] : size == 1 ? total[1] : total[0];
+    if constexpr (RAGGED == kRaggedRows) {  // exclusive scan of the groups' counts
+      const int own = size == 2 ? sum[2] : size == 1 ? sum[1] : sum[0];
+      int run = own;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += v;
+        const int v = __shfl_up_sync(0xffffffffu, run, off);
+        if (lane >= off) run += v;
       }
-      int run = incl - sum;
+      run -= own;
       for (int g = lo; g < hi; ++g) {
-        const int c = tile_start[g];
-        tile_start[g] = run;
-        run += c;
+        tab[2 * p.G + g] = run;
+        run += tiles_of<EPI>(p, tab[2 * g + 1], lr);
       }
-      total = __shfl_sync(0xffffffffu, incl, 31);
-    } else {
-      total = p.G * tiles_of<RAGGED, EPI>(p, p.rows);
     }
     if (lane == 0) {
-      const int r = total % n_clusters;
-      const int split = p.partial != nullptr ? split_of(r, n_clusters, p.kb_typ, p.rows_typ) : 1;
-      sched_smem[0] = split > 1 ? total - r : total;
+      const int r = all % n_clusters;
+      const int split = p.partial != nullptr ? split_of(r, n_clusters, p.kb_typ, min(p.rows_typ, 1 << lr)) : 1;
+      sched_smem[0] = split > 1 ? all - r : all;
       sched_smem[1] = split;
-      sched_smem[2] = split > 1 ? total - r + r * split : total;
+      sched_smem[2] = split > 1 ? all - r + r * split : all;
+      sched_smem[3] = lr;
     }
   }
   tc_fence_before();
@@ -543,7 +656,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   cluster_sync();  // both CTAs' barriers and tensor memory are ready before either is used remotely
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const Sched sc = {sched_smem[0], sched_smem[1], sched_smem[2]};
+  Sched sc;
+  sc.full = sched_smem[0], sc.split = sched_smem[1], sc.items = sched_smem[2], sc.lr = sched_smem[3];
+  sc.ct = (p.cols + kTile - 1) / kTile;
+  sc.per = RAGGED == kRaggedRows ? 1 : tiles_of<EPI>(p, p.rows, sc.lr);
+  sc.step = step_of<EPI>(p.rows, (p.rows + (1 << sc.lr) - 1) >> sc.lr, sc.lr);
+  sc.inv_split = __frcp_rn((float)sc.split), sc.inv_band = __frcp_rn((float)(kBand * sc.ct)), sc.inv_per = __frcp_rn((float)sc.per);
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer (both CTAs)
@@ -551,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       uint32_t it = 0;
       bool ok = true;
       for (int i = cluster_id; i < sc.items && ok; i += n_clusters) {
-        const Item x = item_of<RAGGED, EPI>(p, tile_start, sc, i);
+        const Item x = item_of<RAGGED, EPI>(p, tab, sc, i);
         const int half = half_of(x.nr);
         const int box = B_MN ? 0 : box_of(half);
         const CUtensorMap* bmap = &p.b[box];
@@ -617,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       uint32_t it = 0, use = 0;
       bool ok = true;
       for (int i = cluster_id; i < sc.items && ok; i += n_clusters) {
-        const Item x = item_of<RAGGED, EPI>(p, tile_start, sc, i);
+        const Item x = item_of<RAGGED, EPI>(p, tab, sc, i);
         const uint32_t idesc = p.idesc | ((uint32_t)(2 * half_of(x.nr)) >> 3 << 17) | (16u << 24);
         int kb = x.kb0;
         do {  // one use of an accumulator: the whole item, or one drain's K blocks; at least one
@@ -675,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       uint32_t it = 0, phases = 0;
       bool ok = true;
       for (int i = cluster_id; i < sc.items && ok; i += n_clusters) {
-        const Item x = item_of<RAGGED, EPI>(p, tile_start, sc, i);
+        const Item x = item_of<RAGGED, EPI>(p, tab, sc, i);
         const int count = x.kb1 - x.kb0, kx = (x.kb1 - 1) * kBK;
         it += count;
         if (count <= 0 || !ragged_tail(x.krows, kx)) continue;
@@ -701,118 +819,101 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   } else {
     // ------------------------------------------------------------------ epilogue (warps 2..9, both CTAs)
     const int q = warp & 3;         // TMEM lane quarter this warp may read
-    const int h = (warp - 2) >> 2;  // which 128 of the tile's rows
+    const int h = (warp - 2) >> 2;  // which half of the tile's rows, in chunks of 32
     uint32_t use = 0;
     bool ok = true;
-    Staging st = {staging + (warp - 2) * 4 * kChunkBytes, staging_bar + 2 * (warp - 2), 0};
+    Staging st = {staging + (warp - 2) * staging_of(EPI), staging_bar + 2 * (warp - 2), 0};
     for (int i = cluster_id; i < sc.items && ok; i += n_clusters) {
-      const Item x = item_of<RAGGED, EPI>(p, tile_start, sc, i);
+      const Item x = item_of<RAGGED, EPI>(p, tab, sc, i);
       const int col = x.ct * kTile + (int)rank * 128 + q * 32 + lane;
       const bool none = x.kb1 <= x.kb0;
       const bool split = x.slot >= 0;
       float* mine = split ? part_ptr(p, x.slot, sc.split, x.part, (int)rank) + q * 32 + lane : nullptr;
       // chunks of 32 rows with valid rows; none of a staged epilogue where no column is valid
-      const int chunks = kStaged && col - lane >= p.ld ? 0 : max(0, min(4, (x.nr - h * 128 + 31) / 32));
-      if constexpr (kPromote) {
+      const int all = (x.nr + 31) / 32, first = h * ((all + 1) / 2);
+      const int chunks = by_tma(EPI) && col - lane >= p.ld ? 0 : h == 0 ? (all + 1) / 2 : all / 2;
+      const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16) + first * 32;
+      // what becomes of rows j0 + [0, nj) in v
+      auto finish = [&](const float (&v)[32], int c) {
+        const int j0 = (first + c) * 32;
+        const int nj = min(32, x.nr - j0);
+        if (split) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j < nj) __stcg(mine + (size_t)(j0 + j) * 128, v[j]);
+        } else if constexpr (kStaged) {
+          const bool more = c + 1 < chunks;
+          if (more) fetch<EPI>(p, st, x.g, x.r0 + j0 + 32, col - lane, lane);
+          ok = emit_staged<EPI>(p, x, st, more ? 1 : 0, v, j0, nj, col, lane) && ok;
+        } else if constexpr (EPI == kGrad) {
+          emit_grad(p, x, st, v, j0, nj, col, lane);
+        } else {
+          emit<RAGGED, EPI>(p, x, st.buf, v, j0, nj, col, lane);
+        }
+      };
+      if (kPromote && x.kb1 - x.kb0 > kPromoteBlocks) {
         float acc[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int j = 0; j < 32; ++j) acc[c][j] = 0.0f;
-        int kb = x.kb0;
-        do {
+        for (int kb = x.kb0; kb < x.kb1; kb += kPromoteBlocks, ++use) {
           const uint32_t buf = use & 1;
           ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (use >> 1) & 1, kWaitLimitNs));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + buf * kTile + h * 128;
-          if (!none) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              if (c < chunks) {
+          for (int c = 0; c < 4; ++c) {
+            if (c < chunks) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {  // 16 at a time: 128 sums and 16 addends fit the registers
-                  uint32_t r[16];
-                  tmem_ld_32x32b_x16(tacc + c * 32 + u * 16, r);
-                  tmem_ld_wait();
+              for (int u = 0; u < 2; ++u) {  // 16 at a time: 128 sums and 16 addends fit the registers
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(tlane + buf * kTile + c * 32 + u * 16, r);
+                tmem_ld_wait();
 #pragma unroll
-                  for (int j = 0; j < 16; ++j) acc[c][u * 16 + j] += __uint_as_float(r[j]);
-                }
+                for (int j = 0; j < 16; ++j) acc[c][u * 16 + j] += __uint_as_float(r[j]);
               }
             }
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
-          ++use;
-          kb += kPromoteBlocks;
-        } while (kb < x.kb1);
+          if (lane == 0) mbar_arrive_even(&acc_empty[buf]);
+        }
         if (!ok) {
           if (lane == 0) set_error(p.err, kErrTimeout);
           break;
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int j0 = h * 128 + c * 32;
-          const int nj = min(32, x.nr - j0);
-          if (c < chunks) {
-            if (!split) {
-              emit<RAGGED, EPI>(p, x, acc[c], j0, nj, col);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (j < nj) __stcg(mine + (size_t)(j0 + j) * 128, acc[c][j]);
-            }
-          }
-        }
+        for (int c = 0; c < 4; ++c)
+          if (c < chunks) finish(acc[c], c);
       } else {
         const uint32_t buf = use & 1;
         if constexpr (kStaged)
-          if (!split && chunks > 0) fetch<EPI>(p, st, x.g, x.r0 + h * 128, col - lane, lane);
+          if (!split && chunks > 0) fetch<EPI>(p, st, x.g, x.r0 + first * 32, col - lane, lane);
         ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (use >> 1) & 1, kWaitLimitNs));
         if (!ok) {
           if (lane == 0) set_error(p.err, kErrTimeout);
           break;
         }
         tc_fence_after();
-        const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + buf * kTile + h * 128;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-          const int j0 = h * 128 + c * 32;
-          const int nj = min(32, x.nr - j0);
-          float v[32];
-          if (!none) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(tacc + c * 32, r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-          }
-          if (c == chunks - 1) {  // the accumulator has been read
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(tlane + buf * kTile + c * 32, r);
+          tmem_ld_wait();
+          if (c + 1 == chunks) {  // the accumulator has been read
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+            if (lane == 0) mbar_arrive_even(&acc_empty[buf]);
           }
-          if (!split) {
-            if constexpr (kStaged) {
-              const bool more = c + 1 < chunks;
-              if (more) fetch<EPI>(p, st, x.g, x.r0 + j0 + 32, col - lane, lane);
-              ok = emit_staged<EPI>(p, x, st, more ? 1 : 0, v, j0, nj, col, lane) && ok;
-            } else {
-              emit<RAGGED, EPI>(p, x, v, j0, nj, col);
-            }
-          } else {
+          float v[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j < nj) __stcg(mine + (size_t)(j0 + j) * 128, v[j]);
-          }
+          for (int j = 0; j < 32; ++j) v[j] = none ? 0.0f : __uint_as_float(r[j]);
+          finish(v, c);
         }
         if (chunks == 0) {
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+          if (lane == 0) mbar_arrive_even(&acc_empty[buf]);
         }
         ++use;
       }
@@ -829,21 +930,22 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           if (lane == 0) *counter = 0;
 #pragma unroll 1
           for (int c = 0; c < chunks; ++c) {
-            const int j0 = h * 128 + c * 32;
+            const int j0 = (first + c) * 32;
             const int nj = min(32, x.nr - j0);
             if constexpr (kStaged) fetch<EPI>(p, st, x.g, x.r0 + j0, col - lane, lane);
-            const float* first = part_ptr(p, x.slot, sc.split, 0, (int)rank) + (size_t)j0 * 128 + q * 32 + lane;
+            const float* part0 = part_ptr(p, x.slot, sc.split, 0, (int)rank) + (size_t)j0 * 128 + q * 32 + lane;
             const size_t pitch = 2 * (size_t)p.prows * 128;
             float v[32];
-            if (nj <= 4) add_parts<4, 16>(first, pitch, sc.split, nj, v);
-            else add_parts<16, 4>(first, pitch, sc.split, nj, v);
+            if (nj <= 4) add_parts<4, 8>(part0, pitch, sc.split, nj, v);
+            else add_parts<8, 4>(part0, pitch, sc.split, nj, v);
             if constexpr (kStaged) ok = emit_staged<EPI>(p, x, st, 0, v, j0, nj, col, lane) && ok;
-            else emit<RAGGED, EPI>(p, x, v, j0, nj, col);
+            else if constexpr (EPI == kGrad) emit_grad(p, x, st, v, j0, nj, col, lane);
+            else emit<RAGGED, EPI>(p, x, st.buf, v, j0, nj, col, lane);
           }
         }
       }
     }
-    if constexpr (kStaged) {
+    if constexpr (by_tma(EPI)) {
       if (!ok && lane == 0) set_error(p.err, kErrTimeout);
       if (lane == 0) bulk_wait();
     }
@@ -879,21 +981,21 @@ inline EncodeFn encode_fn() {
   return fn;
 }
 
-// 16-bit row-major [groups, rows, inner] tensor, box of box_inner elements x box_rows rows of one group,
-// 128-byte swizzle for an operand (64 elements), none for a staged chunk (32); what lies past inner or
-// rows reads as zero and is not written.  inner is a multiple of 8.
-inline bool make_map(CUtensorMap* m, bool bf16, const void* base, uint64_t inner, uint64_t rows, uint64_t groups,
-                     uint32_t box_rows, uint32_t box_inner = 64) {
+// row-major [groups, rows, inner] tensor, box of box_inner elements x box_rows rows of one group, 128-byte
+// swizzle for an operand, none for what the epilogue loads or stores; what lies past inner or rows reads as
+// zero and is not written.  A row is a multiple of 16 bytes.
+inline bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t rows,
+                     uint64_t groups, uint32_t box_inner, uint32_t box_rows, bool swizzle) {
   EncodeFn enc = encode_fn();
   if (enc == nullptr || inner == 0 || rows == 0 || groups == 0) return false;
+  const uint64_t size = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
   cuuint64_t dims[3] = {inner, rows, groups};
-  cuuint64_t strides[2] = {inner * 2, inner * rows * 2};
+  cuuint64_t strides[2] = {inner * size, inner * rows * size};
   cuuint32_t box[3] = {box_inner, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base),
-             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             box_inner == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc(m, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // the current device is one this library runs on
@@ -923,15 +1025,17 @@ template <bool A_MN, bool B_MN>
 bool set_operands(Params& p, const OperandHost& a, const OperandHost& b, bool bf16) {
   const uint32_t ty = bf16 ? 1u : 0u;
   p.idesc = (1u << 4) | (ty << 7) | (ty << 10) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16);
-  if (!make_map(&p.a, bf16, a.base, a.inner, a.rows, a.groups, A_MN ? 64 : 128)) return false;
+  const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  if (!make_map(&p.a, type, a.base, a.inner, a.rows, a.groups, 64, A_MN ? 64 : 128, true)) return false;
   for (int i = 0; i < (B_MN ? 1 : kBoxes); ++i)
-    if (!make_map(&p.b[i], bf16, b.base, b.inner, b.rows, b.groups, B_MN ? 64 : box_rows(i))) return false;
+    if (!make_map(&p.b[i], type, b.base, b.inner, b.rows, b.groups, 64, B_MN ? 64 : box_rows(i), true)) return false;
   return true;
 }
 
-// a staged epilogue's map of a 16-bit [groups, rows, inner] tensor
-inline bool set_chunks(CUtensorMap* m, const OperandHost& t) {
-  return make_map(m, false, t.base, t.inner, t.rows, t.groups, 32, 32);
+// the epilogue's map of a [groups, rows, inner] tensor of 16 bits, or of fp32
+inline bool set_chunks(CUtensorMap* m, const OperandHost& t, bool fp32 = false, uint32_t rows = 32) {
+  return make_map(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, t.base, t.inner, t.rows,
+                  t.groups, 32, rows, false);
 }
 
 template <bool A_MN, bool B_MN, int RAGGED, int EPI>
