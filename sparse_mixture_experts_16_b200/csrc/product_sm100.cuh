@@ -211,18 +211,16 @@ struct Sched {
 // through memory, 16 rows x 4 parts at a time, a memory latency or two K blocks each.  Without the split
 // a one-token product of 4 experts x [5760, 2880] leaves 3/4 of the clusters idle in its second round;
 // full tiles of 256 rows are worth splitting only along a long K.
-__device__ __forceinline__ int split_of(int r, int clusters, int kb, int rows) {
-  if (r <= 0) return 1;
-  const int most = min(kMaxSplit, min(kb / 2, kMaxParts / r));
+__device__ __forceinline__ int split_of(int r, int clusters, int kb, int rows, int lane) {  // a whole warp
+  const int most = r > 0 ? min(kMaxSplit, min(kb / 2, kMaxParts / r)) : 1;
   const float groups = (float)((rows + 15) / 32);  // of 16 rows, per warp
-  int best = 1;
+  const int s = lane + 1;
   float cost = 1e30f;
-  for (int s = 1; s <= most || s == 1; ++s) {
-    const float rounds = (float)((r * s + clusters - 1) / clusters);
-    const float c = rounds * ((float)kb / (float)s + 4.0f) + (s > 1 ? 4.0f + 2.0f * groups * (float)((s + 3) / 4) : 0.0f);
-    if (c < cost) cost = c, best = s;
-  }
-  return best;
+  if (s <= most || s == 1)
+    cost = (float)((r * s + clusters - 1) / clusters) * ((float)kb / (float)s + 4.0f) +
+           (s > 1 ? 4.0f + 2.0f * groups * (float)((s + 3) / 4) : 0.0f);
+  const uint32_t least = __reduce_min_sync(0xffffffffu, __float_as_uint(cost));  // of positive numbers
+  return __ffs(__ballot_sync(0xffffffffu, __float_as_uint(cost) == least));
 }
 
 struct Item {
@@ -594,6 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     tmem_alloc_pair(tmem_slot, 2 * kTile);
     tmem_relinquish_pair();
   }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // both CTAs' barriers and tensor memory are ready before either is used remotely
+  tc_fence_after();
   pdl_wait();
   pdl_trigger();
   if constexpr (RAGGED != kDense) {
@@ -642,19 +644,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         run += tiles_of<EPI>(p, tab[2 * g + 1], lr);
       }
     }
+    const int r = all % n_clusters;
+    const int split = split_of(r, n_clusters, p.kb_typ, min(p.rows_typ, 1 << lr), lane);
     if (lane == 0) {
-      const int r = all % n_clusters;
-      const int split = p.partial != nullptr ? split_of(r, n_clusters, p.kb_typ, min(p.rows_typ, 1 << lr)) : 1;
       sched_smem[0] = split > 1 ? all - r : all;
       sched_smem[1] = split;
       sched_smem[2] = split > 1 ? all - r + r * split : all;
       sched_smem[3] = lr;
     }
   }
-  tc_fence_before();
-  __syncwarp();
-  cluster_sync();  // both CTAs' barriers and tensor memory are ready before either is used remotely
-  tc_fence_after();
+  __syncthreads();
   const uint32_t tmem_base = *tmem_slot;
   Sched sc;
   sc.full = sched_smem[0], sc.split = sched_smem[1], sc.items = sched_smem[2], sc.lr = sched_smem[3];
