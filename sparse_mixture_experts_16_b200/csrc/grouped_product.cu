@@ -110,10 +110,9 @@ moe_status_t moe_grouped_gemm_wgrad(const void* dy, const void* x, const int32_t
   p.cols = K;
   p.kb_typ = (M / E + kBK - 1) / kBK;  // the mean segment
   p.rows_typ = N;
-  p.out = dw;
   p.ld = K;
   const OperandHost out = {dw, (uint64_t)K, (uint64_t)N, (uint64_t)E};
-  if (!set_chunks(&p.out_map, out, true) || !set_chunks(&p.out_lo_map, out, true, 16)) return MOE_ERR_CUDA;
+  if (!set_output(p, out)) return MOE_ERR_CUDA;
   p.withhold_first_load = test_withhold_this_launch() ? 1 : 0;
   set_workspace(p, ws, partial_rows(N));
   const OperandHost a = {x, (uint64_t)K, (uint64_t)M, 1};

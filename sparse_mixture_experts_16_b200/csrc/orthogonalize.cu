@@ -9,20 +9,21 @@
 //
 // Each step is three launches of the kernel of product_sm100.cuh over a batch of matrices:
 //     A  = X X^T  (M <= N) or X^T X       symmetric: the lower tiles, each stored with its mirror image
-//     P  = b A + c A A                    symmetric
-//     X <- a X + P X  or  a X + X P
+//     P  = a I + b A + c A A              symmetric
+//     X <- P X  or  X P
 // 3 m^2 n + m^3 products per step for n = max(M, N), a quarter to a third below the plain form's.
 //
 // Numerics.  Operands are fp16 scaled by 2^12 (not bf16: the same tensor-core rate with 1/8 of the
-// rounding; |X| <= 1.2025, |A| <= 1.45, |P| <= 2.81, so nothing overflows, and values down to 2^-36
+// rounding; |X| <= 1.2025, |A| <= 1.45, |P| <= 3.4445, so nothing overflows, and values down to 2^-36
 // keep a bit).  A singular value v grows by up to a^steps = 485, and so does what rounding adds along
 // directions that the matrix does not have; gradients of experts with few tokens are of such low
-// rank.  X is therefore kept as hi + lo * 2^-11 (22 bits): the tensor core multiplies hi, and the
-// term a X, which alone carries small singular values, adds both.  In a simulation of exactly these
-// roundings over ten spectra (full rank, rank 8 and 64, polynomial and geometric decay, one huge
-// entry) the result is 2e-4 to 1.7e-3 off in the 2-norm, less than its rounding to bf16; without lo
-// 4e-2, with bf16 operands 3e-1 (rank 8).  P uses the rounded A in both terms: its error is then that
-// of a nearby X, which the iteration damps (with the unrounded A in b A it is twice as large).
+// rank.  X is therefore kept as hi + lo * 2^-11 (22 bits): the tensor core multiplies hi, and
+// a lo * 2^-11 is added to the product.  The last step multiplies hi alone: what it leaves out grows
+// by a once.  In a simulation of exactly these roundings over nine spectra (full rank, rank 8 and 64,
+// polynomial and geometric decay, one huge entry) the result is 4e-4 to 1.7e-3 off in the 2-norm, no
+// more than its rounding to bf16; without lo 4e-2, without lo in the last two steps 2.9e-3, with bf16
+// operands 3e-1 (rank 8).  P uses the rounded A in both terms: its error is then that of a nearby X,
+// which the iteration damps (with the unrounded A in b A it is twice as large).
 // The norm is summed in 64 bits, so fp32 inputs of any magnitude neither overflow nor vanish.
 #include "product_sm100.cuh"
 
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kPrepThreads) scale_kernel(const T* __restrict
     const unsigned r = i / per, c = (i - r * per) * 8;
     const T* at = m + (long long)r * N + c;
     float v[8];
-    if (wide) load8(at, v);
+    if (wide && (int)c < N) load8(at, v);
     else load8_tail(at, min(8, N - (int)c), v);
     uint32_t h[4], l[4];
 #pragma unroll
@@ -158,14 +159,14 @@ constexpr long long kBatchBytes = 1LL << 30;
 bool layout_of(int B, int M, int N, Layout& l) {
   if (B <= 0 || M <= 0 || N <= 0 || M > 65536 || N > 65536) return false;
   l.low = M < N ? M : N;
-  l.lp = (l.low + 7) / 8 * 8;
-  l.np = (N + 7) / 8 * 8;
+  l.lp = (l.low + 15) / 16 * 16;
+  l.np = (N + 15) / 16 * 16;
   const long long rt = (l.low + kTile - 1) / kTile, tiles = rt * (rt + 1) / 2;
   long long batch = (kTargetTiles + tiles - 1) / tiles;
   const long long fits = kBatchBytes / (6LL * M * l.np);
   if (batch > fits) batch = fits > 1 ? fits : 1;
   l.batch = B < batch ? B : (int)batch;
-  l.prows = partial_rows(M);
+  l.prows = partial_rows(M > l.np ? M : l.np);
   size_t at = align_up(kPartialOffset + partial_bytes(l.prows), 256);
   auto take = [&](size_t bytes) {
     const size_t was = at;
@@ -212,8 +213,7 @@ cudaError_t iterate(int count, int M, int N, int steps, const Layout& l, uint16_
   base.counters = reinterpret_cast<int*>(b + kWsHeader);
   base.partial = reinterpret_cast<float*>(b + kPartialOffset);
   base.prows = l.prows;
-  const OperandHost olo = {b + l.lo, (uint64_t)l.np, (uint64_t)M, G};
-  if (!set_chunks(&base.src_lo_map, olo) || !set_chunks(&base.out_lo_map, olo)) return cudaErrorInvalidValue;
+  uint16_t* lo = reinterpret_cast<uint16_t*>(b + l.lo);
   uint16_t* hi[2] = {reinterpret_cast<uint16_t*>(b + l.hi0), reinterpret_cast<uint16_t*>(b + l.hi1)};
   uint16_t* gram = reinterpret_cast<uint16_t*>(b + l.gram);
   uint16_t* poly = reinterpret_cast<uint16_t*>(b + l.poly);
@@ -249,34 +249,44 @@ cudaError_t iterate(int count, int M, int N, int steps, const Layout& l, uint16_
     p.kb_typ = (p.K + kBK - 1) / kBK;
     p.rows_typ = l.low;
     p.out = poly;
-    if (!set_chunks(&p.src_map, og) || !set_chunks(&p.out_map, op)) return cudaErrorInvalidValue;
+    p.src = gram;
     p.c0 = kNsB;
     p.c1 = kNsC * kUnscale;
+    p.c2 = kNsA * kScale;
     if (!set_operands<false, false>(p, og, og, false)) return cudaErrorInvalidValue;
     if ((e = launch<false, false, kDense, kPoly>(p, s)) != cudaSuccess) return e;
 
     p = base;
-    p.rows = M;
-    p.cols = l.np;
-    p.ld = l.np;
     p.K = l.lp;
     p.kb_typ = (p.K + kBK - 1) / kBK;
-    p.rows_typ = M;
-    p.out = last ? out : hi[(k + 1) & 1];
-    p.cols_out = N;
-    p.store_out = N % 8 == 0 ? 1 : 0;
-    const OperandHost onext = {p.out, (uint64_t)(last ? N : l.np), (uint64_t)M, G};
-    if (!set_chunks(&p.src_map, ox)) return cudaErrorInvalidValue;
-    if ((!last || p.store_out) && !set_chunks(&p.out_map, onext)) return cudaErrorInvalidValue;
-    p.c0 = kNsA;
-    p.c1 = kUnscale;
-    p.c2 = kUnscale;
-    if (tall) {  // X P: P's rows are the columns, X's rows the rows
-      if (!set_operands<false, false>(p, op, ox, false)) return cudaErrorInvalidValue;
-      e = last ? launch<false, false, kDense, kApplyLast>(p, s) : launch<false, false, kDense, kApply>(p, s);
-    } else {     // P X: X is contracted over its rows
-      if (!set_operands<true, false>(p, ox, op, false)) return cudaErrorInvalidValue;
-      e = last ? launch<true, false, kDense, kApplyLast>(p, s) : launch<true, false, kDense, kApply>(p, s);
+    if (last) {
+      p.rows = p.rows_typ = M;
+      p.cols = l.np;
+      p.cols_out = N;
+      p.out = out;
+      p.c1 = kUnscale * kUnscale;
+      if (tall) {  // X P: P's rows are the columns, X's rows the rows
+        if (!set_operands<false, false>(p, op, ox, false)) return cudaErrorInvalidValue;
+        e = launch<false, false, kDense, kApplyLast>(p, s);
+      } else {     // P X: X is contracted over its rows
+        if (!set_operands<true, false>(p, ox, op, false)) return cudaErrorInvalidValue;
+        e = launch<true, false, kDense, kApplyLast>(p, s);
+      }
+    } else {       // the same with rows and columns exchanged
+      p.rows = p.rows_typ = p.ld = l.np;
+      p.cols = M;
+      p.src = lo;
+      p.out = hi[(k + 1) & 1];
+      p.out_lo = k < steps - 2 ? lo : nullptr;
+      p.c0 = kNsA / 2048.0f;
+      p.c1 = kUnscale;
+      if (tall) {
+        if (!set_operands<false, false>(p, ox, op, false)) return cudaErrorInvalidValue;
+        e = launch<false, false, kDense, kApply>(p, s);
+      } else {
+        if (!set_operands<false, true>(p, op, ox, false)) return cudaErrorInvalidValue;
+        e = launch<false, true, kDense, kApply>(p, s);
+      }
     }
     if (e != cudaSuccess) return e;
   }

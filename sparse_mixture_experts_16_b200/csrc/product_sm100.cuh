@@ -55,15 +55,15 @@ enum Epilogue {
   kOut16 = 0,     // out = bf16 or fp16
   kOut32 = 1,     // out = fp32, promoted accumulation
   kGram = 2,      // symmetric: out = fp16(acc * c1), and its mirror image
-  kPoly = 3,      // symmetric: out = fp16(c0 * src + acc * c1), and its mirror image
-  kApply = 4,     // x = c0 * (src + src_lo / 2048) + acc * c1; out = fp16(x), out_lo = fp16(2048 (x - out))
-  kApplyLast = 5, // out = bf16(the same x * c2), rows of cols_out elements
+  kPoly = 3,      // symmetric: out = fp16(c0 * src + acc * c1), c2 added on the diagonal, and its mirror image
+  kApply = 4,     // x = acc * c1 + src * c0; out = fp16(x), out_lo = fp16(2048 (x - out)): out[column][row]
+  kApplyLast = 5, // out = bf16(acc * c1), rows of cols_out elements
   kGrad = 6       // as kOut32, of groups of equal rows: leaves by TMA
 };
 
 constexpr int kTile = 256;               // rows (N) and columns (M) of a pair's tile
 constexpr int kBK = 64;                  // K per stage
-constexpr int kStages = 6;               // 5 where the epilogue stages 16-bit tiles (stages_of)
+constexpr int kStages = 6;               // 5 beside kGrad's staging (stages_of)
 constexpr int kThreads = 352;
 constexpr int kEpiWarps = 8;
 constexpr int kTileA = 128 * kBK * 2;    // 16 KB: this CTA's columns
@@ -71,13 +71,12 @@ constexpr int kTileB = 128 * kBK * 2;    // 16 KB: this CTA's rows, at most
 constexpr int kStageBytes = kTileA + kTileB;
 constexpr int kPromoteBlocks = 8;        // K blocks per accumulator drain (512 k)
 constexpr int kMaxGroups = 1024;
-constexpr int kBarBytes = 384;  // 3 per stage, 4 of the accumulators, 16 of the staging, the tensor memory's address
+constexpr int kBarBytes = 256;  // 3 per stage, 4 of the accumulators, the tensor memory's address
 constexpr int kChunkBytes = 32 * 32 * 2;  // 32 rows x 32 columns of 16 bits: what a warp's epilogue handles at a time
-constexpr bool staged(int epi) { return epi == kPoly || epi == kApply || epi == kApplyLast; }  // adds to 16-bit tiles
-constexpr bool by_tma(int epi) { return staged(epi) || epi == kGrad; }  // loads or stores by TMA
-// staging per epilogue warp: two buffers of two 16-bit arrays or of fp32 by TMA; one for a 16-bit transposition
-constexpr int staging_of(int epi) { return by_tma(epi) ? 4 * kChunkBytes : epi == kOut16 || epi == kGram ? kChunkBytes : 0; }
-constexpr int stages_of(int epi) { return by_tma(epi) ? kStages - 1 : kStages; }
+// shared memory of an epilogue warp: a chunk of 16 bits turned from columns to rows; kGrad: two chunks of fp32
+// on their way out
+constexpr int staging_of(int epi) { return epi == kGrad ? 4 * kChunkBytes : epi == kOut32 || epi == kApply ? 0 : kChunkBytes; }
+constexpr int stages_of(int epi) { return epi == kGrad ? kStages - 1 : kStages; }
 // groups whose segments' bounds are held in shared memory (kGrad: what the staging leaves room for)
 constexpr int table_groups(int epi) { return epi == kGrad ? 190 : kMaxGroups; }
 constexpr size_t smem_bytes(int epi) {
@@ -105,21 +104,18 @@ struct alignas(64) Params {
   CUtensorMap a;          // K-major: box 64 k x 128 columns; MN-major: box 64 columns x 64 k
   CUtensorMap b[kBoxes];  // K-major: boxes of 64 k x box_rows(i) rows; MN-major (the first): 64 rows x 64 k
   const int32_t* offsets;  // kRaggedRows / kRaggedK: segment bounds [G + 1]
-  // boxes of 32 columns x 32 rows: src, src_lo, out and out_lo of the staged epilogues, out of kGrad, whose
-  // out_lo_map is out in boxes of 16 rows
-  CUtensorMap src_map;
-  CUtensorMap src_lo_map;
-  CUtensorMap out_map;
-  CUtensorMap out_lo_map;
-  int store_out;           // kApplyLast: out_map holds out (its pitch allows it)
+  CUtensorMap out_map;     // kGrad: out in boxes of 32 columns x 32 and x 16 rows
+  CUtensorMap out16_map;
   int G;                   // groups
   int M_total;             // rows of the ragged tensor
   int rows, cols, K;       // rows (not kRaggedRows), columns and K (not kRaggedK) of a group
   uint32_t idesc;          // instruction descriptor without M and N
   int out_bf16;            // kOut16: bf16 instead of fp16
-  int ld;                  // row pitch of src / out of the Newton-Schulz epilogues
+  int ld;                  // row pitch of src, src_lo, out, out_lo of the Newton-Schulz epilogues
   int cols_out;            // kApplyLast: row pitch of out, columns that are stored
   void* out;
+  uint16_t* out_lo;        // kApply; null: not kept
+  const uint16_t* src;     // kPoly: symmetric; kApply: of out's layout, may be out_lo
   float c0, c1, c2;
   float* partial;
   int* counters;
@@ -265,13 +261,11 @@ __device__ __forceinline__ int divide(int n, int d, float inv, int& rem) {
 }
 
 // Rows of a tile of a group.  They are dealt evenly over its rt row tiles, in 16s: a tile of few rows costs
-// nearly half a full one, for the columns' operand comes in whole.  The symmetric products keep square
-// tiles, and what leaves in boxes of 32 rows tiles of whole boxes.
+// nearly half a full one, for the columns' operand comes in whole.  The symmetric products keep square tiles.
 template <int EPI>
 __device__ __forceinline__ int step_of(int rows, int rt, int lr) {
-  constexpr int kUnit = staged(EPI) ? 32 : 16;
   if (symmetric(EPI) || rt == 1) return 1 << lr;
-  return ((rows + rt - 1) / rt + kUnit - 1) / kUnit * kUnit;
+  return ((rows + rt - 1) / rt + 15) / 16 * 16;
 }
 
 // tab: kRaggedRows, kRaggedK: first row and rows of each group; kRaggedRows: then the first tile of each
@@ -352,17 +346,6 @@ __device__ __forceinline__ bool ragged_tail(int krows, int kx) { return kx + kBK
 __device__ __forceinline__ uint16_t half_bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
 __device__ __forceinline__ float half_val(uint16_t b) { return __half2float(__ushort_as_half(b)); }
 
-// Symmetric products: the values of rows row_in + 2 i and + 1, column col, packed in w[i], as row col,
-// columns row_in ..
-__device__ __forceinline__ void mirror(const Params& p, const Item& x, const uint32_t (&w)[16], int row_in, int col) {
-  if (!x.triangle || x.rt == x.ct || col >= p.rows) return;
-  uint16_t* m = static_cast<uint16_t*>(p.out) + ((long long)x.g * p.rows + col) * p.ld + row_in;
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-    if (row_in + 8 * u + 8 <= p.ld)
-      *reinterpret_cast<uint4*>(m + 8 * u) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
-}
-
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -372,16 +355,80 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One warp's 32 rows x 32 columns, v[j] = accumulator of row j0 + j and column col (this lane's); nj rows
-// are valid.  16-bit results are packed by pairs of rows, turned through shared memory and stored 16 bytes
-// a lane: a store per element made this half of the epilogue's 6000 cycles a tile.  A row of 32 fp32 is one
-// store of a warp.
+__device__ __forceinline__ float2 unpack_half(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+// 32 bytes of a lane: one sector
+__device__ __forceinline__ void load_sector(const uint16_t* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void store_sector(uint16_t* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Where the output's rows are the tile's columns (kApply by the choice of operands, the symmetric products by
+// symmetry) a lane's 32 values are 64 contiguous bytes of its own row, and nothing goes through shared
+// memory, whose bandwidth the operands of the MMAs use up: chunks staged there took 10000 to 18000 cycles a
+// tile beside 16400 of MMA (K = 2048).  Pitches are multiples of 16 elements, so whole sectors move, and so
+// are the rows of a tile or they end in zeros.
+__device__ __forceinline__ long long lane_row(const Params& p, const Item& x, int rows, int j0, int col) {
+  return ((long long)x.g * rows + col) * p.ld + x.r0 + j0;
+}
+__device__ __forceinline__ void store_lane_row(uint16_t* o, const uint32_t (&w)[16], int nj) {
+  store_sector(o, w);
+  if (nj > 16) store_sector(o + 16, w + 8);
+}
+
+// what kPoly and kApply add to a chunk: read one chunk ahead
+template <int EPI>
+__device__ __forceinline__ void load_addend(const Params& p, const Item& x, uint32_t (&s)[16], int j0, int col) {
+  const int rows = EPI == kPoly ? p.rows : p.cols;
+  if (j0 >= x.nr || col >= rows) return;
+  const uint16_t* at = p.src + lane_row(p, x, rows, j0, col);
+  load_sector(at, s);
+  if (x.nr - j0 > 16) load_sector(at + 16, s + 8);
+}
+
+// A warp's 16-bit chunk, w[i] = rows 2 i and 2 i + 1 of this lane's column, turned through shared memory and
+// stored 16 bytes a lane (a store per element made this half of the epilogue's 6000 cycles a tile).  o: the
+// first row's place at the chunk's first column; limit: columns that exist from there on, a multiple of 8.
+__device__ __forceinline__ void store_turned(uint16_t* o, int pitch, uint8_t* buf, const uint32_t (&w)[16], int nj,
+                                             int limit, int lane) {
+  uint32_t* b = reinterpret_cast<uint32_t*>(buf);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) b[i * 32 + lane] = w[i];
+  __syncwarp();
+  const int c8 = (lane & 3) * 8;  // eight columns of a pair of rows
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int pair = (lane >> 2) + 8 * i;
+    const uint4 l = *reinterpret_cast<const uint4*>(b + pair * 32 + c8);
+    const uint4 h = *reinterpret_cast<const uint4*>(b + pair * 32 + c8 + 4);
+    if (c8 < limit) {
+      uint16_t* at = o + (long long)(2 * pair) * pitch + c8;
+      if (2 * pair < nj)
+        *reinterpret_cast<uint4*>(at) = make_uint4(__byte_perm(l.x, l.y, 0x5410), __byte_perm(l.z, l.w, 0x5410),
+                                                   __byte_perm(h.x, h.y, 0x5410), __byte_perm(h.z, h.w, 0x5410));
+      if (2 * pair + 1 < nj)
+        *reinterpret_cast<uint4*>(at + pitch) = make_uint4(__byte_perm(l.x, l.y, 0x7632), __byte_perm(l.z, l.w, 0x7632),
+                                                           __byte_perm(h.x, h.y, 0x7632), __byte_perm(h.z, h.w, 0x7632));
+    }
+  }
+  __syncwarp();  // the buffer is written again
+}
+
+// One warp's 32 rows x 32 columns, v[j] = accumulator of row j0 + j and column col (this lane's), s its
+// addend; nj rows are valid.
 template <int RAGGED, int EPI>
-__device__ __forceinline__ void emit(const Params& p, const Item& x, uint8_t* buf, const float (&v)[32], int j0, int nj,
-                                     int col, int lane) {
+__device__ __forceinline__ void emit(const Params& p, const Item& x, uint8_t* buf, const float (&v)[32],
+                                     const uint32_t (&s)[16], int j0, int nj, int col, int lane) {
   const int row_in = x.r0 + j0;  // row within the group
   const long long row = (RAGGED == kRaggedRows ? (long long)x.row0 : (long long)x.g * p.rows) + row_in;
-  if constexpr (EPI == kOut32) {
+  uint16_t* const out = static_cast<uint16_t*>(p.out);
+  if constexpr (EPI == kOut32) {  // a row of 32 columns is one store of a warp
     if (col >= p.cols) return;
     float* o = static_cast<float*>(p.out) + row * p.cols + col;
     if (nj == 32) {
@@ -392,120 +439,60 @@ __device__ __forceinline__ void emit(const Params& p, const Item& x, uint8_t* bu
       for (int j = 0; j < 32; ++j)
         if (j < nj) o[(long long)j * p.cols] = v[j];
     }
-  } else {  // kOut16, kGram
-    uint32_t w[16];
-    if (EPI == kOut16 && p.out_bf16) {
+  } else if constexpr (EPI == kApply) {
+    if (col >= p.cols) return;
+    uint32_t hi[16], lo[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 16; ++i) {  // two at a time: only the conversions of pairs run at full rate
+      const float2 a = unpack_half(s[i]);
+      const float w0 = v[2 * i] * p.c1 + a.x * p.c0, w1 = v[2 * i + 1] * p.c1 + a.y * p.c0;
+      hi[i] = pack_half(w0, w1);
+      const float2 f = unpack_half(hi[i]);
+      lo[i] = pack_half((w0 - f.x) * 2048.0f, (w1 - f.y) * 2048.0f);
+    }
+    const long long at = lane_row(p, x, p.cols, j0, col);
+    store_lane_row(out + at, hi, nj);
+    if (p.out_lo != nullptr) store_lane_row(p.out_lo + at, lo, nj);
+  } else {
+    uint32_t w[16];
+    if constexpr (EPI == kPoly) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 a = unpack_half(s[i]);
+        w[i] = pack_half(v[2 * i] * p.c1 + a.x * p.c0 + (row_in + 2 * i == col ? p.c2 : 0.0f),
+                         v[2 * i + 1] * p.c1 + a.y * p.c0 + (row_in + 2 * i + 1 == col ? p.c2 : 0.0f));
+      }
+    } else if (EPI == kApplyLast || (EPI == kOut16 && p.out_bf16)) {
+      const float c = EPI == kApplyLast ? p.c1 : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i] * c, v[2 * i + 1] * c);
     } else {
       const float c = EPI == kGram ? p.c1 : 1.0f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) w[i] = pack_half(v[2 * i] * c, v[2 * i + 1] * c);
     }
-    uint32_t* b = reinterpret_cast<uint32_t*>(buf);
+    if constexpr (symmetric(EPI)) {  // the tile's transpose, and itself where no other tile is its transpose
+      if (col < p.rows) store_lane_row(out + lane_row(p, x, p.rows, j0, col), w, nj);
+      if (x.triangle && x.rt != x.ct) store_turned(out + row * p.ld + col - lane, p.ld, buf, w, nj, p.ld - (col - lane), lane);
+    } else {
+      const int pitch = EPI == kOut16 ? p.cols : p.cols_out, limit = pitch - (col - lane);
+      uint16_t* o = out + row * pitch + col - lane;
+      if (EPI == kOut16 || (pitch & 7) == 0) {
+        store_turned(o, pitch, buf, w, nj, limit, lane);
+      } else if (lane < limit) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) b[i * 32 + lane] = w[i];
-    __syncwarp();
-    const int pitch = EPI == kGram ? p.ld : p.cols;
-    const int c8 = (lane & 3) * 8;  // eight columns of a pair of rows
-    uint16_t* o = static_cast<uint16_t*>(p.out) + row * pitch + (col - lane + c8);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int pair = (lane >> 2) + 8 * i;
-      const uint4 l = *reinterpret_cast<const uint4*>(b + pair * 32 + c8);
-      const uint4 h = *reinterpret_cast<const uint4*>(b + pair * 32 + c8 + 4);
-      if (col - lane + c8 < pitch) {
-        if (2 * pair < nj)
-          *reinterpret_cast<uint4*>(o + (long long)(2 * pair) * pitch) =
-              make_uint4(__byte_perm(l.x, l.y, 0x5410), __byte_perm(l.z, l.w, 0x5410), __byte_perm(h.x, h.y, 0x5410),
-                         __byte_perm(h.z, h.w, 0x5410));
-        if (2 * pair + 1 < nj)
-          *reinterpret_cast<uint4*>(o + (long long)(2 * pair + 1) * pitch) =
-              make_uint4(__byte_perm(l.x, l.y, 0x7632), __byte_perm(l.z, l.w, 0x7632), __byte_perm(h.x, h.y, 0x7632),
-                         __byte_perm(h.z, h.w, 0x7632));
-      }
-    }
-    __syncwarp();  // the buffer is written again
-    if constexpr (EPI == kGram) mirror(p, x, w, row_in, col);
-  }
-}
-
-// The staged epilogues' chunks.  What they add to the accumulators (src, and src_lo for X) comes by TMA
-// into one of the warp's two buffers, the result takes its place there and leaves by TMA, while the next
-// chunk's addends come into the other buffer.  (With two-byte loads and stores of the lanes the same
-// launch took 590 us instead of 430 on 8 matrices of 2048 x 7168, K = 2048; its MMAs take 300.)
-struct Staging {
-  uint8_t* buf;    // 2 x (2 KB of src and out, 2 KB of their low-order parts)
-  uint64_t* bar;   // 2: landed
-  uint32_t n;      // chunks fetched so far
-};
-
-// lane 0: fetch the chunk at (col0, row) into the next buffer, whose last store was the last but one
-template <int EPI>
-__device__ __forceinline__ void fetch(const Params& p, Staging& st, int g, int row, int col0, int lane) {
-  if (lane == 0) {
-    uint8_t* b = st.buf + (st.n & 1) * 2 * kChunkBytes;
-    uint64_t* bar = &st.bar[st.n & 1];
-    bulk_wait_read();
-    mbar_arrive_expect_tx(bar, EPI == kPoly ? kChunkBytes : 2 * kChunkBytes);
-    tma_3d(&p.src_map, bar, b, col0, row, g);
-    if constexpr (EPI != kPoly) tma_3d(&p.src_lo_map, bar, b + kChunkBytes, col0, row, g);
-  }
-  ++st.n;
-}
-
-// the chunk fetched `ago` fetches before the last one has landed (false: the wait expired); adds v, stores
-template <int EPI>
-__device__ __forceinline__ bool emit_staged(const Params& p, const Item& x, const Staging& st, int ago,
-                                            const float (&v)[32], int j0, int nj, int col, int lane) {
-  const uint32_t n = st.n - 1 - ago;
-  uint16_t* hi = reinterpret_cast<uint16_t*>(st.buf + (n & 1) * 2 * kChunkBytes) + lane;
-  uint16_t* lo = hi + kChunkBytes / 2;
-  if (!__all_sync(0xffffffffu, mbar_wait(&st.bar[n & 1], (n >> 1) & 1, kWaitLimitNs))) return false;
-  const int row = x.r0 + j0, col0 = col - lane;
-  if constexpr (EPI == kPoly) {
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      w[i] = pack_half(v[2 * i] * p.c1 + p.c0 * half_val(hi[i * 64]), v[2 * i + 1] * p.c1 + p.c0 * half_val(hi[i * 64 + 32]));
-      hi[i * 64] = (uint16_t)w[i];
-      hi[i * 64 + 32] = (uint16_t)(w[i] >> 16);
-    }
-    mirror(p, x, w, row, col);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float w = p.c0 * (half_val(hi[j * 32]) + half_val(lo[j * 32]) * (1.0f / 2048.0f)) + v[j] * p.c1;
-      if constexpr (EPI == kApply) {
-        const uint16_t h = half_bits(w);
-        hi[j * 32] = h;
-        lo[j * 32] = half_bits((w - half_val(h)) * 2048.0f);
-      } else {
-        const uint16_t b = __bfloat16_as_ushort(__float2bfloat16_rn(w * p.c2));
-        if (p.store_out) {
-          hi[j * 32] = b;
-        } else if (j < nj && col < p.cols_out) {
-          static_cast<uint16_t*>(p.out)[((long long)x.g * p.rows + row + j) * p.cols_out + col] = b;
-        }
+        for (int j = 0; j < 32; ++j)
+          if (j < nj) o[(long long)j * pitch + lane] = (uint16_t)(w[j / 2] >> 16 * (j & 1));
       }
     }
   }
-  fence_async();
-  __syncwarp();
-  if (lane == 0) {
-    uint8_t* b = st.buf + (n & 1) * 2 * kChunkBytes;
-    if (EPI != kApplyLast || p.store_out) tma_store_3d(&p.out_map, b, col0, row, x.g);
-    if constexpr (EPI == kApply) tma_store_3d(&p.out_lo_map, b + kChunkBytes, col0, row, x.g);
-    bulk_commit();
-  }
-  return true;
 }
 
 // kGrad: rows j0 + [0, nj) leave as one box of 32 x 32 (16 x 32 at the end of a tile) from the buffer
 // whose last store was the last but one; what lies past the matrix is not written
-__device__ __forceinline__ void emit_grad(const Params& p, const Item& x, Staging& st, const float (&v)[32], int j0,
-                                          int nj, int col, int lane) {
-  float* b = reinterpret_cast<float*>(st.buf + (st.n++ & 1) * 2 * kChunkBytes);
+__device__ __forceinline__ void emit_grad(const Params& p, const Item& x, uint8_t* buf, uint32_t& stored,
+                                          const float (&v)[32], int j0, int nj, int col, int lane) {
+  float* b = reinterpret_cast<float*>(buf + (stored++ & 1) * 2 * kChunkBytes);
   if (lane == 0) bulk_wait_read_but_one();
   __syncwarp();
 #pragma unroll
@@ -513,7 +500,7 @@ __device__ __forceinline__ void emit_grad(const Params& p, const Item& x, Stagin
   fence_async();
   __syncwarp();
   if (lane == 0) {
-    tma_store_3d(nj > 16 ? &p.out_map : &p.out_lo_map, b, col - lane, x.r0 + j0, x.g);
+    tma_store_3d(nj > 16 ? &p.out_map : &p.out16_map, b, col - lane, x.r0 + j0, x.g);
     bulk_commit();
   }
 }
@@ -551,7 +538,7 @@ __device__ __forceinline__ float* part_ptr(const Params& p, int slot, int split,
 // ------------------------------------------------------------------------------ the kernel
 template <bool A_MN, bool B_MN, int RAGGED, int EPI>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p) {
-  constexpr bool kPromote = EPI == kOut32 || EPI == kGrad, kStaged = staged(EPI);
+  constexpr bool kPromote = EPI == kOut32 || EPI == kGrad, kAdds = EPI == kPoly || EPI == kApply;
   constexpr int kStages = stages_of(EPI);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -560,8 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   uint64_t* acc_full = empty + kStages;                                       // both CTAs: accumulator ready
   uint64_t* acc_empty = acc_full + 2;                                         // even CTA: both epilogues done
   uint64_t* tail_bar = acc_empty + 2;                                         // kRaggedK: this CTA's tail block landed
-  uint64_t* staging_bar = tail_bar + kStages;                                 // staged: two per epilogue warp
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(staging_bar + 2 * kEpiWarps);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail_bar + kStages);
   uint8_t* staging = smem + kStages * kStageBytes + kBarBytes;
   int* sched_smem = reinterpret_cast<int*>(staging + kEpiWarps * staging_of(EPI));
   int* tab = sched_smem + 4;  // item_of's table
@@ -583,7 +569,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 2 * kEpiWarps);
     }
-    for (int b = 0; b < 2 * kEpiWarps; ++b) mbar_init(&staging_bar[b], 1);
     fence_barrier_init();
     prefetch_tensormap(&p.a);
     for (int i = 0; i < (B_MN ? 1 : kBoxes); ++i) prefetch_tensormap(&p.b[i]);
@@ -821,16 +806,18 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int h = (warp - 2) >> 2;  // which half of the tile's rows, in chunks of 32
     uint32_t use = 0;
     bool ok = true;
-    Staging st = {staging + (warp - 2) * staging_of(EPI), staging_bar + 2 * (warp - 2), 0};
+uint8_t* const buf0 = staging + (warp - 2) * staging_of(EPI);
+    uint32_t stored = 0;  // kGrad: chunks stored, alternately from two buffers
+    uint32_t next[16];    // the next chunk's addend
     for (int i = cluster_id; i < sc.items && ok; i += n_clusters) {
       const Item x = item_of<RAGGED, EPI>(p, tab, sc, i);
       const int col = x.ct * kTile + (int)rank * 128 + q * 32 + lane;
       const bool none = x.kb1 <= x.kb0;
       const bool split = x.slot >= 0;
       float* mine = split ? part_ptr(p, x.slot, sc.split, x.part, (int)rank) + q * 32 + lane : nullptr;
-      // chunks of 32 rows with valid rows; none of a staged epilogue where no column is valid
+      // chunks of 32 rows with valid rows; of kGrad none where no column is valid
       const int all = (x.nr + 31) / 32, first = h * ((all + 1) / 2);
-      const int chunks = by_tma(EPI) && col - lane >= p.ld ? 0 : h == 0 ? (all + 1) / 2 : all / 2;
+      const int chunks = EPI == kGrad && col - lane >= p.ld ? 0 : h == 0 ? (all + 1) / 2 : all / 2;
       const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16) + first * 32;
       // what becomes of rows j0 + [0, nj) in v
       auto finish = [&](const float (&v)[32], int c) {
@@ -840,14 +827,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if (j < nj) __stcg(mine + (size_t)(j0 + j) * 128, v[j]);
-        } else if constexpr (kStaged) {
-          const bool more = c + 1 < chunks;
-          if (more) fetch<EPI>(p, st, x.g, x.r0 + j0 + 32, col - lane, lane);
-          ok = emit_staged<EPI>(p, x, st, more ? 1 : 0, v, j0, nj, col, lane) && ok;
         } else if constexpr (EPI == kGrad) {
-          emit_grad(p, x, st, v, j0, nj, col, lane);
+          emit_grad(p, x, buf0, stored, v, j0, nj, col, lane);
+        } else if constexpr (kAdds) {
+          uint32_t s[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) s[j] = next[j];
+          load_addend<EPI>(p, x, next, c + 1 < chunks ? j0 + 32 : x.nr, col);
+          emit<RAGGED, EPI>(p, x, buf0, v, s, j0, nj, col, lane);
         } else {
-          emit<RAGGED, EPI>(p, x, st.buf, v, j0, nj, col, lane);
+          emit<RAGGED, EPI>(p, x, buf0, v, next, j0, nj, col, lane);
         }
       };
       if (kPromote && x.kb1 - x.kb0 > kPromoteBlocks) {
@@ -887,8 +876,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           if (c < chunks) finish(acc[c], c);
       } else {
         const uint32_t buf = use & 1;
-        if constexpr (kStaged)
-          if (!split && chunks > 0) fetch<EPI>(p, st, x.g, x.r0 + first * 32, col - lane, lane);
+        if constexpr (kAdds)
+          if (!split && chunks > 0) load_addend<EPI>(p, x, next, first * 32, col);
         ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (use >> 1) & 1, kWaitLimitNs));
         if (!ok) {
           if (lane == 0) set_error(p.err, kErrTimeout);
@@ -931,23 +920,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           for (int c = 0; c < chunks; ++c) {
             const int j0 = (first + c) * 32;
             const int nj = min(32, x.nr - j0);
-            if constexpr (kStaged) fetch<EPI>(p, st, x.g, x.r0 + j0, col - lane, lane);
+            if constexpr (kAdds) load_addend<EPI>(p, x, next, j0, col);
             const float* part0 = part_ptr(p, x.slot, sc.split, 0, (int)rank) + (size_t)j0 * 128 + q * 32 + lane;
             const size_t pitch = 2 * (size_t)p.prows * 128;
             float v[32];
             if (nj <= 4) add_parts<4, 8>(part0, pitch, sc.split, nj, v);
             else add_parts<8, 4>(part0, pitch, sc.split, nj, v);
-            if constexpr (kStaged) ok = emit_staged<EPI>(p, x, st, 0, v, j0, nj, col, lane) && ok;
-            else if constexpr (EPI == kGrad) emit_grad(p, x, st, v, j0, nj, col, lane);
-            else emit<RAGGED, EPI>(p, x, st.buf, v, j0, nj, col, lane);
+            if constexpr (EPI == kGrad) emit_grad(p, x, buf0, stored, v, j0, nj, col, lane);
+            else emit<RAGGED, EPI>(p, x, buf0, v, next, j0, nj, col, lane);
           }
         }
       }
     }
-    if constexpr (by_tma(EPI)) {
-      if (!ok && lane == 0) set_error(p.err, kErrTimeout);
+    if constexpr (EPI == kGrad)
       if (lane == 0) bulk_wait();
-    }
   }
 
   tc_fence_before();
@@ -1031,10 +1017,10 @@ bool set_operands(Params& p, const OperandHost& a, const OperandHost& b, bool bf
   return true;
 }
 
-// the epilogue's map of a [groups, rows, inner] tensor of 16 bits, or of fp32
-inline bool set_chunks(CUtensorMap* m, const OperandHost& t, bool fp32 = false, uint32_t rows = 32) {
-  return make_map(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, t.base, t.inner, t.rows,
-                  t.groups, 32, rows, false);
+// kGrad's maps of its fp32 [groups, rows, inner] output
+inline bool set_output(Params& p, const OperandHost& t) {
+  return make_map(&p.out_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, t.base, t.inner, t.rows, t.groups, 32, 32, false) &&
+         make_map(&p.out16_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, t.base, t.inner, t.rows, t.groups, 32, 16, false);
 }
 
 template <bool A_MN, bool B_MN, int RAGGED, int EPI>
