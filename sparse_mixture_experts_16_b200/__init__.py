@@ -326,26 +326,27 @@ def _ws_size(name, *sizes):
     return getattr(lib(), name)(*sizes)
 
 
-def _product_ws(ws, need, device):
+def _product_ws(ws, need, index):
     """``ws`` if it is large enough, else a zero-filled workspace of ``need`` bytes."""
     import torch
 
     if ws is None or ws.numel() < need:
-        return torch.zeros(need, dtype=torch.uint8, device=device)
-    if not (ws.dtype is torch.uint8 and ws.is_cuda and ws.is_contiguous() and ws.device == device):
-        raise ValueError(f"ws: expected a contiguous uint8 tensor on {device}")
+        return torch.zeros(need, dtype=torch.uint8, device=torch.device("cuda", index))
+    if not (ws.dtype is torch.uint8 and ws.is_cuda and ws.is_contiguous() and ws.get_device() == index):
+        raise ValueError(f"ws: expected a contiguous uint8 tensor on cuda:{index}")
     return ws
 
 
-def _launch(name, device, stream, *args):
-    """Calls the C entry point with ``args`` and the stream on ``device``."""
+def _launch(name, index, stream, *args):
+    """Calls the C entry point with ``args`` and the stream on CUDA device ``index``."""
     import torch
 
-    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if torch.cuda.current_device() == device.index:
+    # the handle of torch's current stream; a Stream object of it costs 2 us
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
         status = getattr(lib(), name)(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = getattr(lib(), name)(*args, handle)
     if status != 0:
         raise MoeError(status, name)
@@ -370,13 +371,12 @@ def _rows_product(name, rows, offsets, w, contracted, wide, out, out_dtype, ws, 
         out_dtype = dtype if out is None else out.dtype
     if out_dtype is not dtype and out_dtype is not torch.float32:
         raise ValueError(f"out_dtype: expected {dtype} or torch.float32, got {out_dtype}")
-    device = rows.device
     if out is None:
-        out = torch.empty(M, sizes[wide], dtype=out_dtype, device=device)
+        out = torch.empty(M, sizes[wide], dtype=out_dtype, device=rows.device)
     else:
         _need_at(out, out_dtype, (M, sizes[wide]), index, "out")
-    ws = _product_ws(ws, _ws_size("moe_grouped_gemm_workspace_size", M), device)
-    _launch(name, device, stream, rows.data_ptr(), offsets.data_ptr(), w.data_ptr(), M, E, N, K, _dtype_code(dtype),
+    ws = _product_ws(ws, _ws_size("moe_grouped_gemm_workspace_size", M), index)
+    _launch(name, index, stream, rows.data_ptr(), offsets.data_ptr(), w.data_ptr(), M, E, N, K, _dtype_code(dtype),
             _dtype_code(out_dtype), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out, ws
 
@@ -410,13 +410,12 @@ def moe_grouped_gemm_wgrad(dy, x, offsets, out=None, ws=None, stream=None):
     _need_at(dy, dtype, (M, N), index, "dy")
     _need_at(x, dtype, (M, K), index, "x")
     _need_at(offsets, torch.int32, (E + 1,), index, "offsets")
-    device = dy.device
     if out is None:
-        out = torch.empty(E, N, K, dtype=torch.float32, device=device)
+        out = torch.empty(E, N, K, dtype=torch.float32, device=dy.device)
     else:
         _need_at(out, torch.float32, (E, N, K), index, "out")
-    ws = _product_ws(ws, _ws_size("moe_grouped_gemm_wgrad_workspace_size", N), device)
-    _launch("moe_grouped_gemm_wgrad", device, stream, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), M, E, N, K,
+    ws = _product_ws(ws, _ws_size("moe_grouped_gemm_wgrad_workspace_size", N), index)
+    _launch("moe_grouped_gemm_wgrad", index, stream, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), M, E, N, K,
             _dtype_code(dtype), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out, ws
 
@@ -434,10 +433,9 @@ def moe_orthogonalize(g, steps=5, out=None, ws=None, stream=None):
         raise ValueError("g: expected [..., M, N]")
     index = g.get_device()
     _need_at(g, g.dtype, g.shape, index, "g")
-    device = g.device
     M, N = g.shape[-2:]
     if out is None:
-        out = torch.empty(g.shape, dtype=torch.bfloat16, device=device)
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
     else:
         _need_at(out, torch.bfloat16, g.shape, index, "out")
     B = g.numel() // (M * N) if M * N else 0
@@ -446,8 +444,8 @@ def moe_orthogonalize(g, steps=5, out=None, ws=None, stream=None):
     need = _ws_size("moe_orthogonalize_workspace_size", B, M, N)
     if need == 0:
         raise MoeError(2, "moe_orthogonalize_workspace_size")
-    ws = _product_ws(ws, need, device)
-    _launch("moe_orthogonalize", device, stream, g.data_ptr(), _dtype_code(g.dtype), B, M, N, int(steps),
+    ws = _product_ws(ws, need, index)
+    _launch("moe_orthogonalize", index, stream, g.data_ptr(), _dtype_code(g.dtype), B, M, N, int(steps),
             out.data_ptr(), ws.data_ptr(), ws.numel())
     return out, ws
 
