@@ -595,7 +595,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   __syncwarp();
   cluster_sync();  // both CTAs' barriers and tensor memory are ready before either is used remotely
   tc_fence_after();
-  pdl_wait();
+  // Segments are read from memory that the kernel before may have written; the schedule of equal groups is
+  // not, so there the producer and the epilogue wait before their own first access: 118 -> 111 us for
+  // 16 x [512, 256].
+  if constexpr (RAGGED != kDense) pdl_wait();
   pdl_trigger();
   if constexpr (RAGGED != kDense) {
     for (int g = threadIdx.x; g < p.G; g += kThreads) {
@@ -668,6 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       bool ok = true;
       for (int i = cluster_id; i < sc.items && ok; i += n_clusters) {
         const Item x = item_of<RAGGED, EPI>(p, tab, sc, i);
+        if (RAGGED == kDense && i == cluster_id) pdl_wait();
         const int half = half_of(x.nr);
         const int box = B_MN ? 0 : box_of(half);
         const CUtensorMap* bmap = &p.b[box];
@@ -825,6 +829,7 @@ uint8_t* const buf0 = staging + (warp - 2) * staging_of(EPI);
     uint32_t next[16];    // the next chunk's addend
     for (int i = cluster_id; i < sc.items && ok; i += n_clusters) {
       const Item x = item_of<RAGGED, EPI>(p, tab, sc, i);
+      if (RAGGED == kDense && i == cluster_id) pdl_wait();
       const int col = x.ct * kTile + (int)rank * 128 + q * 32 + lane;
       const bool none = x.kb1 <= x.kb0;
       const bool split = x.slot >= 0;
