@@ -108,6 +108,8 @@ struct alignas(64) Params {
   CUtensorMap out16_map;
   int G;                   // groups
   int M_total;             // rows of the ragged tensor
+  int ct, lr;              // column tiles; a tile has at most 2^lr rows
+  int tiles, split;        // not kRaggedRows: tiles, parts of each tile of the last round
   int rows, cols, K;       // rows (not kRaggedRows), columns and K (not kRaggedK) of a group
   uint32_t idesc;          // instruction descriptor without M and N
   int out_bf16;            // kOut16: bf16 instead of fp16
@@ -209,26 +211,38 @@ struct Sched {
   int full;   // tiles dealt whole
   int split;  // parts of each later tile
   int items;
-  int lr;     // a tile has at most 2^lr rows
-  int ct;     // column tiles
   int per;    // not kRaggedRows: tiles of a group, rows of a tile
   int step;
   float inv_split, inv_band, inv_per;
 };
 
-// Parts of each of the r < clusters tiles of the last round.  Cost in K blocks (of about 0.3 us): rounds
-// of parts, each with a fixed share for filling the pipeline and for the epilogue; then the parts' way
-// through memory, 16 rows x 4 parts at a time, a memory latency or two K blocks each.  Without the split
-// a one-token product of 4 experts x [5760, 2880] leaves 3/4 of the clusters idle in its second round;
-// full tiles of 256 rows are worth splitting only along a long K.
-__device__ __forceinline__ int split_of(int r, int clusters, int kb, int rows, int lane) {  // a whole warp
-  const int most = r > 0 ? min(kMaxSplit, min(kb / 2, kMaxParts / r)) : 1;
-  const float groups = (float)((rows + 15) / 32);  // of 16 rows, per warp
+// The size of the tiles and the parts into which those of the last, partly filled round are split along K.
+// Cost in K blocks of a full tile (some 550 cycles): a block of a tile of few rows costs half as much, as
+// the columns' operand comes in whole; a tile has a fixed share for filling the pipeline, the last one its
+// epilogue; parts travel through memory, 8 rows x 8 parts at a time and a memory latency each.  Without the
+// split a one-token product of 4 experts x [5760, 2880] leaves 3/4 of the clusters idle in its second round;
+// with tiles of 256 rows only, one of 8 experts x 194 rows, [1000, 520], leaves 42 of 74 idle.  The host
+// chooses both (choose); where segments decide how many tiles there are it takes the mean segment's size for
+// the tiles, and the parts are chosen on the device.
+__host__ __device__ inline float cost_of(int tiles, int clusters, int kb, int rows, int s) {
+  const int full = tiles / clusters, r = tiles - full * clusters;
+  const float block = 0.5f + (float)rows * (1.0f / 512.0f);
+  float cost = (float)full * ((float)kb * block + 3.0f) + (float)rows * (1.0f / 64.0f);
+  if (r > 0) {
+    const int rounds = (r * s + clusters - 1) / clusters;
+    cost += (float)rounds * ((float)kb / (float)s * block + 4.0f);
+    if (s > 1) cost += 4.0f + 2.0f * (float)((rows + 15) / 16 * ((s + 7) / 8));
+  }
+  return cost;
+}
+__host__ __device__ inline int most_parts(int r, int kb) {
+  const int a = kb / 2 < kMaxSplit ? kb / 2 : kMaxSplit, b = r > 0 ? kMaxParts / r : 1;
+  return a < b ? a : b;
+}
+// parts of each of the r tiles of the last round; a whole warp
+__device__ __forceinline__ int split_of(int r, int clusters, int kb, int rows, int lane) {
   const int s = lane + 1;
-  float cost = 1e30f;
-  if (s <= most || s == 1)
-    cost = (float)((r * s + clusters - 1) / clusters) * ((float)kb / (float)s + 4.0f) +
-           (s > 1 ? 4.0f + 2.0f * groups * (float)((s + 3) / 4) : 0.0f);
+  const float cost = s <= most_parts(r, kb) || s == 1 ? cost_of(r, clusters, kb, rows, s) : 1e30f;
   const uint32_t least = __reduce_min_sync(0xffffffffu, __float_as_uint(cost));  // of positive numbers
   return __ffs(__ballot_sync(0xffffffffu, __float_as_uint(cost) == least));
 }
@@ -252,16 +266,15 @@ __device__ __forceinline__ void segment(const Params& p, int g, int& row0, int& 
   bad = row0 != a || end != b;
 }
 
-// Tiles of a group of `rows` rows, at most 2^lr of them in a tile.  With fewer tiles than clusters the limit
-// is 128 or 64 rows, so that more of the machine takes part and the epilogues get shorter.  Of a symmetric
+// Tiles of a group of `rows` rows, at most 2^lr of them in a tile (256, 128 or 64).  Of a symmetric
 // product only the lower triangle of 256 x 256 tiles is computed, but all of the smaller tiles.
 constexpr int kMostLr = 8, kLeastLr = 6;
 constexpr bool symmetric(int epi) { return epi == kGram || epi == kPoly; }
 template <int EPI>
-__device__ __forceinline__ int tiles_of(const Params& p, int rows, int lr) {
+__host__ __device__ inline int tiles_of(int rows, int ct, int lr) {
   const int rt = (rows + (1 << lr) - 1) >> lr;
   if (symmetric(EPI) && lr == kMostLr) return rt * (rt + 1) / 2;
-  return rt * ((p.cols + kTile - 1) / kTile);
+  return rt * ct;
 }
 
 // n / d for quotients below 2^22, inv = 1 / d: the estimate is off by at most one (every role divides for every
@@ -320,8 +333,8 @@ __device__ __forceinline__ Item item_of(const Params& p, const int* tab, const S
       }
     }
   }
-  const int rt = (rows + (1 << sc.lr) - 1) >> sc.lr;
-  x.triangle = symmetric(EPI) && sc.lr == kMostLr;
+  const int rt = (rows + (1 << p.lr) - 1) >> p.lr;
+  x.triangle = symmetric(EPI) && p.lr == kMostLr;
   if (x.triangle) {
     // lower triangle, row by row
     int r = (int)((sqrtf(8.0f * (float)local + 1.0f) - 1.0f) * 0.5f);
@@ -333,12 +346,12 @@ __device__ __forceinline__ Item item_of(const Params& p, const int* tab, const S
     // bands of 8 row tiles, rows fastest inside a band: the ~74 tiles in flight share about 8 row
     // blocks and 9 column blocks through L2
     int rem, in_band;
-    const int band = divide(local, kBand * sc.ct, sc.inv_band, rem);
+    const int band = divide(local, kBand * p.ct, sc.inv_band, rem);
     const int rb = min(kBand, rt - kBand * band);
     x.ct = divide(rem, rb, __fdividef(1.0f, (float)rb), in_band);
     x.rt = kBand * band + in_band;
   }
-  const int step = RAGGED == kRaggedRows ? step_of<EPI>(rows, rt, sc.lr) : sc.step;
+  const int step = RAGGED == kRaggedRows ? step_of<EPI>(rows, rt, p.lr) : sc.step;
   x.r0 = x.rt * step;
   x.nr = min(step, rows - x.r0);
   const int kb = RAGGED == kRaggedK ? (x.krows + kBK - 1) / kBK : (p.K + kBK - 1) / kBK;
@@ -614,55 +627,40 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   }
   __syncthreads();
   if (warp == 0) {
-    int total[3] = {0, 0, 0};  // tiles of at most 64, 128, 256 rows
-    const int per = (p.G + 31) / 32;  // kRaggedRows: groups of a lane
-    const int lo = min(p.G, lane * per), hi = min(p.G, lo + per);
-    if constexpr (RAGGED == kRaggedRows) {
-      for (int g = lo; g < hi; ++g)
-#pragma unroll
-        for (int u = 0; u < 3; ++u) total[u] += tiles_of<EPI>(p, tab[2 * g + 1], kLeastLr + u);
-    } else {
-#pragma unroll
-      for (int u = 0; u < 3; ++u) total[u] = p.G * tiles_of<EPI>(p, p.rows, kLeastLr + u);
-    }
-    int sum[3] = {total[0], total[1], total[2]};
-    if constexpr (RAGGED == kRaggedRows) {
-#pragma unroll
-      for (int u = 0; u < 3; ++u) total[u] = __reduce_add_sync(0xffffffffu, total[u]);
-    }
-    const int size = total[2] > n_clusters || total[1] > n_clusters ? 2 : total[0] > n_clusters ? 1 : 0;
-    const int lr = kLeastLr + size, all = size == 2 ? total[2] : size == 1 ? total[1] : total[0];
-    if constexpr (RAGGED == kRaggedRows) {  // exclusive scan of the groups' counts
-      const int own = size == 2 ? sum[2] : size == 1 ? sum[1] : sum[0];
+    int all = p.tiles, split = p.split;
+    if constexpr (RAGGED == kRaggedRows) {  // exclusive scan of the groups' tile counts
+      const int per = (p.G + 31) / 32;
+      const int lo = min(p.G, lane * per), hi = min(p.G, lo + per);
+      int own = 0;
+      for (int g = lo; g < hi; ++g) own += tiles_of<EPI>(tab[2 * g + 1], p.ct, p.lr);
       int run = own;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, run, off);
         if (lane >= off) run += v;
       }
+      all = __shfl_sync(0xffffffffu, run, 31);
       run -= own;
       for (int g = lo; g < hi; ++g) {
         tab[2 * p.G + g] = run;
-        run += tiles_of<EPI>(p, tab[2 * g + 1], lr);
+        run += tiles_of<EPI>(tab[2 * g + 1], p.ct, p.lr);
       }
+      split = split_of(all % n_clusters, n_clusters, p.kb_typ, min(p.rows_typ, 1 << p.lr), lane);
     }
-    const int r = all % n_clusters;
-    const int split = split_of(r, n_clusters, p.kb_typ, min(p.rows_typ, 1 << lr), lane);
     if (lane == 0) {
+      const int r = all % n_clusters;
       sched_smem[0] = split > 1 ? all - r : all;
       sched_smem[1] = split;
       sched_smem[2] = split > 1 ? all - r + r * split : all;
-      sched_smem[3] = lr;
     }
   }
   __syncthreads();
   const uint32_t tmem_base = *tmem_slot;
   Sched sc;
-  sc.full = sched_smem[0], sc.split = sched_smem[1], sc.items = sched_smem[2], sc.lr = sched_smem[3];
-  sc.ct = (p.cols + kTile - 1) / kTile;
-  sc.per = RAGGED == kRaggedRows ? 1 : tiles_of<EPI>(p, p.rows, sc.lr);
-  sc.step = step_of<EPI>(p.rows, (p.rows + (1 << sc.lr) - 1) >> sc.lr, sc.lr);
-  sc.inv_split = __frcp_rn((float)sc.split), sc.inv_band = __frcp_rn((float)(kBand * sc.ct)), sc.inv_per = __frcp_rn((float)sc.per);
+  sc.full = sched_smem[0], sc.split = sched_smem[1], sc.items = sched_smem[2];
+  sc.per = RAGGED == kRaggedRows ? 1 : tiles_of<EPI>(p.rows, p.ct, p.lr);
+  sc.step = step_of<EPI>(p.rows, (p.rows + (1 << p.lr) - 1) >> p.lr, p.lr);
+  sc.inv_split = __frcp_rn((float)sc.split), sc.inv_band = __frcp_rn((float)(kBand * p.ct)), sc.inv_per = __frcp_rn((float)sc.per);
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer (both CTAs)
@@ -943,8 +941,8 @@ uint8_t* const buf0 = staging + (warp - 2) * staging_of(EPI);
             const float* part0 = part_ptr(p, x.slot, sc.split, 0, (int)rank) + (size_t)j0 * 128 + q * 32 + lane;
             const size_t pitch = 2 * (size_t)p.prows * 128;
             float v[32];
-            if (nj <= 4) add_parts<4, 8>(part0, pitch, sc.split, nj, v);
-            else add_parts<8, 4>(part0, pitch, sc.split, nj, v);
+            if (nj <= 4) add_parts<4, 16>(part0, pitch, sc.split, nj, v);
+            else add_parts<8, 8>(part0, pitch, sc.split, nj, v);
             if constexpr (EPI == kGrad) emit_grad(p, x, buf0, stored, v, j0, nj, col, lane);
             else emit<RAGGED, EPI>(p, x, buf0, v, next, j0, nj, col, lane);
           }
@@ -1042,8 +1040,31 @@ inline bool set_output(Params& p, const OperandHost& t) {
          make_map(&p.out16_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, t.base, t.inner, t.rows, t.groups, 32, 16, false);
 }
 
+// Tile size and parts (see cost_of).  kRaggedRows: for the mean segment of the groups that have rows
+template <int RAGGED, int EPI>
+void choose(Params& p, int clusters) {
+  p.ct = (p.cols + kTile - 1) / kTile;
+  const int groups = RAGGED == kRaggedRows && p.M_total < p.G ? p.M_total : p.G;
+  const int rows = RAGGED == kRaggedRows ? (p.M_total + groups - 1) / groups : p.rows;
+  float best = 1e30f;
+  for (int lr = kMostLr; lr >= kLeastLr; --lr) {
+    const long long tiles = (long long)groups * tiles_of<EPI>(rows, p.ct, lr);
+    if (lr < kMostLr && tiles > 8 * clusters) break;  // large products: whole tiles
+    const int t = (int)(tiles < (1LL << 30) ? tiles : 1LL << 30), most = most_parts(t % clusters, p.kb_typ);
+    for (int s = 1; s == 1 || s <= most; ++s) {
+      const float c = cost_of(t, clusters, p.kb_typ, rows < 1 << lr ? rows : 1 << lr, s);
+      if (c < best) {
+        best = c;
+        p.lr = lr;
+        p.tiles = t;
+        p.split = s;
+      }
+    }
+  }
+}
+
 template <bool A_MN, bool B_MN, int RAGGED, int EPI>
-cudaError_t launch(const Params& p, cudaStream_t s) {
+cudaError_t launch(Params& p, cudaStream_t s) {
   auto kernel = product_kernel<A_MN, B_MN, RAGGED, EPI>;
   static std::atomic<int> cached[64];  // clusters that fit on the device at once, per device
   int dev = 0;
@@ -1073,6 +1094,7 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
     clusters = clusters > kMaxParts / 2 ? kMaxParts / 2 : clusters;
     if (dev >= 0 && dev < 64) cached[dev].store(clusters);
   }
+  choose<RAGGED, EPI>(p, clusters);
   cfg.gridDim = dim3(2 * clusters);
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, p);
