@@ -231,7 +231,7 @@ __host__ __device__ inline float cost_of(int tiles, int clusters, int kb, int ro
   if (r > 0) {
     const int rounds = (r * s + clusters - 1) / clusters;
     cost += (float)rounds * ((float)kb / (float)s * block + 4.0f);
-    if (s > 1) cost += 4.0f + 2.0f * (float)((rows + 15) / 16 * ((s + 7) / 8));
+    if (s > 1) cost += 8.0f + 2.5f * (float)((rows + 15) / 16 * ((s + 7) / 8));
   }
   return cost;
 }
