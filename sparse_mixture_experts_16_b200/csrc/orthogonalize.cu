@@ -98,6 +98,18 @@ __global__ void __launch_bounds__(kPrepThreads) norm_kernel(const T* __restrict_
   }
 }
 
+// the parts of every matrix's sum of squares; g is on 16 bytes, and so is every matrix whose length is a
+// multiple of 16 bytes
+template <typename T>
+cudaError_t norms_of(const T* g, int count, int M, int N, double* norms, int& parts, cudaStream_t s) {
+  const long long n = (long long)M * N, most = (n + 16 * kPrepThreads - 1) / (16 * kPrepThreads);
+  parts = most < kNormParts ? (int)most : kNormParts;
+  return launch_pdl(norm_kernel<T>, dim3((unsigned)parts, (unsigned)count), dim3(kPrepThreads), 0, s, g, n,
+                    n % (16 / (int)sizeof(T)) == 0 ? 1 : 0, norms);
+}
+
+#include "orthogonalize_small.cuh"
+
 // hi + lo * 2^-11 = 2^12 g / ||g||, rows padded with zeros to the pitch; bound by reading g and writing
 // as many bytes.  `wide`: every row of g starts on 16 bytes.
 template <typename T>
@@ -186,19 +198,14 @@ bool layout_of(int B, int M, int N, Layout& l) {
 
 template <typename T>
 cudaError_t prepare(const T* g, int count, int M, int N, const Layout& l, uint8_t* b, cudaStream_t s) {
-  const long long n = (long long)M * N;
-  long long parts = (n + 16 * kPrepThreads - 1) / (16 * kPrepThreads);
-  if (parts > kNormParts) parts = kNormParts;
   double* norms = reinterpret_cast<double*>(b + l.norms);
-  // g is on 16 bytes: so is every matrix, or every row, whose length is a multiple of 16 bytes
-  const int unit = 16 / (int)sizeof(T);
-  cudaError_t e = launch_pdl(norm_kernel<T>, dim3((unsigned)parts, (unsigned)count), dim3(kPrepThreads), 0, s, g, n,
-                             n % unit == 0 ? 1 : 0, norms);
+  int parts = 0;
+  const cudaError_t e = norms_of(g, count, M, N, norms, parts, s);
   if (e != cudaSuccess) return e;
   long long blocks = ((long long)M * (l.np / 8) + 2 * kPrepThreads - 1) / (2 * kPrepThreads);
   if (blocks > 1024) blocks = 1024;
   return launch_pdl(scale_kernel<T>, dim3((unsigned)blocks, (unsigned)count), dim3(kPrepThreads), 0, s, g, M, N, l.np,
-                    N % 8 == 0 ? 1 : 0, (const double*)norms, (int)parts, reinterpret_cast<uint16_t*>(b + l.hi0),
+                    N % 8 == 0 ? 1 : 0, (const double*)norms, parts, reinterpret_cast<uint16_t*>(b + l.hi0),
                     reinterpret_cast<uint16_t*>(b + l.lo));
 }
 
@@ -299,7 +306,8 @@ extern "C" {
 
 size_t moe_orthogonalize_workspace_size(int B, int M, int N) {
   Layout l;
-  return layout_of(B, M, N, l) ? l.total : 0;
+  if (!layout_of(B, M, N, l)) return 0;
+  return small_side(M, N) ? small_layout(B, M, N).total : l.total;
 }
 
 moe_status_t moe_orthogonalize(const void* g, int g_dtype, int B, int M, int N, int steps, moe_bf16_t* out, void* ws,
@@ -312,11 +320,24 @@ moe_status_t moe_orthogonalize(const void* g, int g_dtype, int B, int M, int N, 
   if (!aligned(g, 16) || !aligned(out, 16) || !aligned(ws, 256)) return MOE_ERR_ALIGNMENT;
   Layout l;
   if (!layout_of(B, M, N, l)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  if (ws_bytes < l.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < moe_orthogonalize_workspace_size(B, M, N)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const moe_status_t st = device_status();
   if (st != MOE_OK) return st;
   uint8_t* b = static_cast<uint8_t*>(ws);
   cudaStream_t s = (cudaStream_t)stream;
+  if (small_side(M, N)) {
+    const SmallLayout sl = small_layout(B, M, N);
+    for (int at = 0; at < B; at += sl.batch) {
+      const int count = B - at < sl.batch ? B - at : sl.batch;
+      const long long skip = (long long)at * M * N;
+      const cudaError_t e =
+          g_dtype == MOE_DTYPE_FP32
+              ? small_orthogonalize(static_cast<const float*>(g) + skip, count, M, N, steps, sl, out + skip, b, s)
+              : small_orthogonalize(static_cast<const uint16_t*>(g) + skip, count, M, N, steps, sl, out + skip, b, s);
+      if (e != cudaSuccess) return launch_status(e);
+    }
+    return MOE_OK;
+  }
   const int rounds = (B + l.batch - 1) / l.batch, most = (B + rounds - 1) / rounds;  // dealt evenly
   for (int at = 0; at < B; at += most) {
     const int count = B - at < most ? B - at : most;

@@ -199,3 +199,73 @@ def test_an_expert_layer_trained_with_it(cuda_device):
             lim = torch.finfo(got.dtype).eps / 2 * ref.abs() + 1.01 * (n + n / 16 + 1) * 2.0 ** -23 * mag
             assert ((got.double() - ref).abs() <= lim + 1e-30).all()
     assert off(u1, iterate(dw1)) < TOL and off(u2, iterate(dw2)) < TOL
+
+
+SMALL = [(1, 1, 300), (3, 2, 2), (2, 24, 3000), (2, 300, 29), (4, 32, 32), (2, 33, 70), (2, 64, 64), (3, 500, 64),
+         (2, 61, 4099), (700, 5, 9), (2, 65, 65)]
+
+
+@pytest.mark.parametrize("steps", [1, 2, 5, 6, 16])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("shape", SMALL, ids=str)
+def test_short_sides(cuda_device, shape, dtype, steps):
+    """a shorter side of at most 64, and up to five steps, has kernels of its own in fp32: below 1e-3 in their
+    simulation, less than the general path's share of the tolerance.  Whatever the steps, the tolerance is
+    that of test_steps; a matrix of one row only scales."""
+    g = gauss(*shape, seed=7).to(dtype)
+    u, ws = moe.moe_orthogonalize(g, steps=steps)
+    assert moe.moe_get_device_error(ws) == 0
+    assert off(u, iterate(g, steps)) < 2.0 ** -8 + 3.4e-3 * max(1, steps / 5)
+
+
+@pytest.mark.parametrize("kind", ["rank1", "rank4", "decay1", "decay2", "decay4", "geometric", "spike", "low_rank_and_noise"])
+@pytest.mark.parametrize("shape", [(2, 64, 64), (2, 32, 900), (2, 900, 64), (2, 40, 70)], ids=str)
+def test_short_sides_of_other_spectra(cuda_device, shape, kind):
+    b, m, n = shape
+    if kind.startswith("rank"):
+        r = int(kind[4:])
+        g = gauss(b, m, r) @ gauss(b, r, n, seed=1)
+    elif kind == "spike":
+        g = gauss(b, m, n)
+        g[:, 3, 5] = 1e4
+    elif kind == "low_rank_and_noise":
+        g = gauss(b, m, 4) @ gauss(b, 4, n, seed=1) + 0.01 * gauss(b, m, n, seed=2)
+    else:
+        u, s, v = torch.linalg.svd(gauss(b, m, n).double(), full_matrices=False)
+        i = torch.arange(s.shape[-1], device="cuda", dtype=torch.float64)
+        s = {"decay1": 1 / (i + 1), "decay2": 1 / (i + 1) ** 2, "decay4": 1 / (i + 1) ** 4, "geometric": 0.7 ** i}[kind]
+        g = (u * s @ v).float()
+    assert off(moe.moe_orthogonalize(g)[0], iterate(g)) < TOL
+
+
+@pytest.mark.parametrize("scale", [1e-42, 1e-30, 1e30])
+@pytest.mark.parametrize("shape", [(2, 20, 90), (2, 90, 50)], ids=str)
+def test_short_sides_of_any_magnitude(cuda_device, shape, scale):
+    g = gauss(*shape) * scale
+    assert off(moe.moe_orthogonalize(g)[0], iterate(g)) < TOL
+
+
+def test_short_sides_zero_nan_and_infinite_matrices_stay_apart(cuda_device):
+    g = gauss(6, 30, 90)
+    g[1] = 0
+    g[3, 2, 5] = float("nan")
+    g[4, 20, 80] = float("inf")
+    u, _ = moe.moe_orthogonalize(g)
+    assert (u[1] == 0).all()
+    assert torch.isnan(u[3]).all() and torch.isnan(u[4]).all()
+    keep = [0, 2, 5]
+    assert off(u[keep], iterate(g[keep])) < TOL
+
+
+def test_short_sides_captured_and_replayed(cuda_device):
+    g = gauss(3, 30, 500)
+    u, ws = moe.moe_orthogonalize(g)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_orthogonalize(g, out=u, ws=ws)
+    for seed in (5, 6):
+        g.copy_(gauss(3, 30, 500, seed=seed))
+        graph.replay()
+        assert off(u, iterate(g)) < TOL
+    again, _ = moe.moe_orthogonalize(g, ws=ws)
+    assert torch.equal(again, u)
