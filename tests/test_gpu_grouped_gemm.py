@@ -326,3 +326,90 @@ def test_withheld_copy_times_out_and_the_context_stays_usable(cuda_device, op):
     assert r.returncode == 0, r.stderr[-3000:]
     res = json.loads([ln for ln in r.stdout.splitlines() if ln.startswith("RESULT ")][-1][len("RESULT "):])
     assert res["first"] == 7 and res["second"] == 0 and res["same"] and res["elapsed"] < 60
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("counts,N,K", [
+    ([511, 513, 1040, 300, 0, 769], 264, 200),   # rows dealt evenly over the tiles
+    ([2049], 520, 72),
+    ([42], 9264, 96), ([42], 96, 9264),          # one tile, split along a long axis
+    ([0, 3, 0, 0, 28, 0, 0, 1], 136, 8136),
+    ([3, 5, 2], 24, 4000),
+    ([1300], 24, 2008),                          # a long segment, a narrow gradient
+    ([190] * 8, 1000, 520),
+], ids=["even", "one", "long_n", "long_k", "ragged_long_k", "few", "narrow", "half_a_round"])
+def test_tiles_and_parts(cuda_device, counts, N, K, out_dtype):
+    check_all(counts, N, K, BF, out_dtype, seed=11)
+
+
+def test_outputs_past_32_bits(cuda_device):
+    """2^31 elements and more: the last rows, the last expert"""
+    M, N, K, E = 70016, 32768, 16, 2
+    x, dy, w = data(9, M, 1, 8, K, BF)[0], None, data(10, 8, E, N, K, BF)[2]
+    off = offsets_of([69000, 1016])
+    y, ws = moe.moe_grouped_gemm(x, off, w)
+    assert y.numel() > 2 ** 31 and moe.moe_get_device_error(ws) == 0
+    for e, s in ((0, slice(0, 40)), (0, slice(68960, 69000)), (1, slice(69000, 69040)), (1, slice(69976, 70016))):
+        a, b = x[s].double(), w[e].double()
+        close(y[s], a @ b.T, a.abs() @ b.abs().T, K)
+    del y
+    E, N, K = 33, 8192, 8192
+    dy, x = data(12, 66, 1, N, K, BF)[1], data(13, 66, 1, N, K, BF)[0]
+    off = offsets_of([2] * E)
+    dw, ws = moe.moe_grouped_gemm_wgrad(dy, x, off)
+    assert dw.numel() > 2 ** 31 and moe.moe_get_device_error(ws) == 0
+    for e in (0, 31, 32):
+        a, b = dy[2 * e:2 * e + 2].double().T, x[2 * e:2 * e + 2].double()
+        close(dw[e], a @ b, a.abs() @ b.abs(), 2)
+
+
+def test_two_streams_with_a_workspace_each(cuda_device):
+    """calls that run side by side, each on its own stream and workspace, give what they give alone"""
+    off = offsets_of([100, 3, 0, 500])
+    x, dy, w = data(14, 603, 4, 520, 776, BF)
+    alone = [moe.moe_grouped_gemm(x, off, w)[0], moe.moe_grouped_gemm_dgrad(dy, off, w)[0],
+             moe.moe_grouped_gemm_wgrad(dy, x, off)[0]]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    wss = [None, None, None]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for i, st in enumerate(streams):
+            call = [lambda **k: moe.moe_grouped_gemm(x, off, w, **k), lambda **k: moe.moe_grouped_gemm_dgrad(dy, off, w, **k),
+                    lambda **k: moe.moe_grouped_gemm_wgrad(dy, x, off, **k)][i]
+            if wss[i] is None:
+                with torch.cuda.stream(st):
+                    out, wss[i] = call()
+            else:
+                with torch.cuda.stream(st):
+                    out, _ = call(ws=wss[i], stream=st)
+            got.append(out)
+        for st in streams:
+            st.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, alone))
+
+
+def test_the_same_rows_in_two_operands(cuda_device):
+    """x and dy may be one tensor, and an output may be reused by the next call"""
+    off = offsets_of([70, 0, 60])
+    x = data(15, 130, 3, 136, 136, BF)[0]
+    dw, ws = moe.moe_grouped_gemm_wgrad(x, x, off)
+    for e, s in ((0, slice(0, 70)), (2, slice(70, 130))):
+        a = x[s].double()
+        close(dw[e], a.T @ a, a.abs().T @ a.abs(), s.stop - s.start)
+    kept = dw.clone()
+    out, _ = moe.moe_grouped_gemm_wgrad(x, x, off, out=dw, ws=ws)
+    assert out is dw and torch.equal(dw, kept)
+
+
+def test_unaligned_and_small_workspaces_are_refused(cuda_device):
+    x, dy, w = data(16, 12, 2, 16, 24, BF)
+    off = offsets_of([5, 7])
+    shifted = torch.empty(12 * 24 + 1, dtype=BF, device="cuda")[1:].view(12, 24)
+    with pytest.raises(moe.MoeError, match="ALIGNMENT"):
+        moe.moe_grouped_gemm(shifted, off, w)
+    small = torch.zeros(1024, dtype=torch.uint8, device="cuda")
+    _, ws = moe.moe_grouped_gemm(x, off, w, ws=small)  # too small: another one comes back
+    assert ws is not small
+    with pytest.raises(ValueError):
+        moe.moe_grouped_gemm(x, off, w, ws=torch.zeros(1 << 26, dtype=torch.float32, device="cuda"))
