@@ -349,13 +349,14 @@ moe_status_t moe_update_router_bias(const int32_t* counts, int E, float gamma, f
  * fp32 additions in a fixed order.  Results do not depend on timing.  dw is overwritten.
  * N and K are multiples of 8 up to 65536; 1 <= E <= 1024; M >= 0 (M = 0: y / dx empty, dw zeros).
  * Any number of rows per segment; few rows (one token) stream the active experts' weights once.
- *   ws: at least the matching _workspace_size() bytes, zero-filled before its first use (later calls of
- *       these entry points and of moe_orthogonalize may share it, one at a time; zero it again after a
- *       MOE_ERR_TIMEOUT); first 256 bytes: the device error word.
+ *   ws: at least the matching _workspace_size() bytes, the first MOE_PRODUCT_WS_ZEROED of them zero-filled
+ *       before its first use (later calls of these entry points and of moe_orthogonalize may share it, one
+ *       at a time; zero them again after a MOE_ERR_TIMEOUT); first 256 bytes: the device error word.
  * ---------------------------------------------------------------------------------------- */
 #define MOE_DTYPE_BF16 0
 #define MOE_DTYPE_FP16 1
 #define MOE_DTYPE_FP32 2
+#define MOE_PRODUCT_WS_ZEROED 8448
 
 size_t moe_grouped_gemm_workspace_size(int M); /* moe_grouped_gemm and moe_grouped_gemm_dgrad */
 moe_status_t moe_grouped_gemm(const void* x, const int32_t* offsets, const void* w, int M, int E, int N, int K,
@@ -376,10 +377,12 @@ moe_status_t moe_grouped_gemm_wgrad(const void* dy, const void* x, const int32_t
  *   g    [B, M, N]  fp32 or bf16 (g_dtype), e.g. dw of moe_grouped_gemm_wgrad, or dgate_up of
  *                   moe_layer_backward seen as [2E, F, D]
  *   out  [B, M, N]  bf16 (must not overlap g)
- * Computed in fp16 with a low-order part of X and fp32 accumulation; the result is rounded to bf16
- * once and is within bf16's rounding of the exact iterate in the 2-norm.  A matrix that holds a NaN or
- * an infinity comes out as NaN; the others of the batch are not affected.  Any sizes 1 <= M, N <=
- * 65536, odd ones too; B >= 0; 1 <= steps <= 16 (5 is usual).
+ * Computed in fp16 with a low-order part of X and fp32 accumulation, or in fp32 where the shorter side is
+ * at most 64; the result is rounded to bf16 once, and after up to 5 steps it is within bf16's rounding of
+ * the exact iterate in the 2-norm.  Each further step multiplies what rounding has added in directions that
+ * the matrix hardly has by up to a.  A matrix that holds a NaN or an infinity comes out as NaN; the others
+ * of the batch are not affected.  Any sizes 1 <= M, N <= 65536, odd ones too; B >= 0; 1 <= steps <= 16 (5 is
+ * usual).
  *   ws: as for moe_grouped_gemm; it holds a few matrices at a time, not the batch.
  * ---------------------------------------------------------------------------------------- */
 size_t moe_orthogonalize_workspace_size(int B, int M, int N); /* 0 if a size is invalid */

@@ -27,6 +27,7 @@ MOE_PATH_PAIR_TILES = 5
 MOE_WEIGHTS_BF16 = 0
 MOE_WEIGHTS_FP8_E4M3 = 1
 MOE_DTYPE_BF16, MOE_DTYPE_FP16, MOE_DTYPE_FP32 = 0, 1, 2
+MOE_PRODUCT_WS_ZEROED = 8448
 
 STATUS = {
     0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHAPE", 3: "MOE_ERR_ALIGNMENT",
@@ -327,22 +328,42 @@ def _ws_size(name, *sizes):
 
 
 def _product_ws(ws, need, index):
-    """``ws`` if it is large enough, else a zero-filled workspace of ``need`` bytes."""
+    """``ws`` if it is large enough, else a new workspace of ``need`` bytes, whose head is zero-filled."""
     import torch
 
     if ws is None or ws.numel() < need:
-        return torch.zeros(need, dtype=torch.uint8, device=torch.device("cuda", index))
+        ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+        ws[:MOE_PRODUCT_WS_ZEROED].zero_()
+        return ws
     if not (ws.dtype is torch.uint8 and ws.is_cuda and ws.is_contiguous() and ws.get_device() == index):
         raise ValueError(f"ws: expected a contiguous uint8 tensor on cuda:{index}")
     return ws
 
 
-def _launch(name, index, stream, *args):
-    """Calls the C entry point with ``args`` and the stream on CUDA device ``index``."""
+def _on_stream(function):
+    """Adds ``stream``: the call runs with it as the current stream, so that what the call allocates and
+    zeroes belongs to it too."""
+    @functools.wraps(function)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return function(*args, **kwargs)
+        import torch
+
+        device = (args[0] if args else next(iter(kwargs.values()))).device
+        if device != stream.device:
+            raise ValueError(f"stream: expected a stream on {device}, got {stream.device}")
+        with torch.cuda.stream(stream):
+            return function(*args, **kwargs)
+
+    return call
+
+
+def _launch(name, index, *args):
+    """Calls the C entry point with ``args`` and the current stream of CUDA device ``index``."""
     import torch
 
     # the handle of torch's current stream; a Stream object of it costs 2 us
-    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(index)
     if torch.cuda.current_device() == index:
         status = getattr(lib(), name)(*args, handle)
     else:
@@ -352,7 +373,7 @@ def _launch(name, index, stream, *args):
         raise MoeError(status, name)
 
 
-def _rows_product(name, rows, offsets, w, contracted, wide, out, out_dtype, ws, stream):
+def _rows_product(name, rows, offsets, w, contracted, wide, out, out_dtype, ws):
     import torch
 
     dtype = rows.dtype
@@ -376,25 +397,28 @@ def _rows_product(name, rows, offsets, w, contracted, wide, out, out_dtype, ws, 
     else:
         _need_at(out, out_dtype, (M, sizes[wide]), index, "out")
     ws = _product_ws(ws, _ws_size("moe_grouped_gemm_workspace_size", M), index)
-    _launch(name, index, stream, rows.data_ptr(), offsets.data_ptr(), w.data_ptr(), M, E, N, K, _dtype_code(dtype),
+    _launch(name, index, rows.data_ptr(), offsets.data_ptr(), w.data_ptr(), M, E, N, K, _dtype_code(dtype),
             _dtype_code(out_dtype), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out, ws
 
 
-def moe_grouped_gemm(x, offsets, w, out=None, out_dtype=None, ws=None, stream=None):
+@_on_stream
+def moe_grouped_gemm(x, offsets, w, out=None, out_dtype=None, ws=None):
     """y[r] = x[r] @ w[e].T for the rows r of each expert segment e: x [M, K], w [E, N, K] (both bf16 or
     both fp16), offsets [E+1] int32 -> (y [M, N] in x's type or ``out_dtype`` = torch.float32, ws).
-    Rows of ``out`` outside every segment are left as they were.  Pass the returned ws (a zero-filled
-    workspace) to later calls to keep it."""
-    return _rows_product("moe_grouped_gemm", x, offsets, w, 2, 1, out, out_dtype, ws, stream)
+    Rows of ``out`` outside every segment are left as they were.  Pass the returned ws to later calls to keep
+    it, one call at a time.  ``stream``: run there; the operands have to be ready on it."""
+    return _rows_product("moe_grouped_gemm", x, offsets, w, 2, 1, out, out_dtype, ws)
 
 
-def moe_grouped_gemm_dgrad(dy, offsets, w, out=None, out_dtype=None, ws=None, stream=None):
+@_on_stream
+def moe_grouped_gemm_dgrad(dy, offsets, w, out=None, out_dtype=None, ws=None):
     """The input gradient of moe_grouped_gemm: dx[r] = dy[r] @ w[e], dy [M, N] -> (dx [M, K], ws)."""
-    return _rows_product("moe_grouped_gemm_dgrad", dy, offsets, w, 1, 2, out, out_dtype, ws, stream)
+    return _rows_product("moe_grouped_gemm_dgrad", dy, offsets, w, 1, 2, out, out_dtype, ws)
 
 
-def moe_grouped_gemm_wgrad(dy, x, offsets, out=None, ws=None, stream=None):
+@_on_stream
+def moe_grouped_gemm_wgrad(dy, x, offsets, out=None, ws=None):
     """The weight gradient of moe_grouped_gemm: dw[e] = dy_e.T @ x_e over the rows of segment e,
     dy [M, N], x [M, K] -> (dw [E, N, K] fp32, ws); zeros for an expert without rows."""
     import torch
@@ -415,12 +439,13 @@ def moe_grouped_gemm_wgrad(dy, x, offsets, out=None, ws=None, stream=None):
     else:
         _need_at(out, torch.float32, (E, N, K), index, "out")
     ws = _product_ws(ws, _ws_size("moe_grouped_gemm_wgrad_workspace_size", N), index)
-    _launch("moe_grouped_gemm_wgrad", index, stream, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), M, E, N, K,
+    _launch("moe_grouped_gemm_wgrad", index, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), M, E, N, K,
             _dtype_code(dtype), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out, ws
 
 
-def moe_orthogonalize(g, steps=5, out=None, ws=None, stream=None):
+@_on_stream
+def moe_orthogonalize(g, steps=5, out=None, ws=None):
     """The Newton-Schulz iterate of each matrix of g [..., M, N] (fp32 or bf16): X = g / ||g||_F, then
     ``steps`` times X <- a X + (b A + c A A) X with A = X X^T -> (bf16 [..., M, N], ws).  Zero matrices
     stay zero.  Typical g: the weight gradients of moe_grouped_gemm_wgrad, or the layer backward's
@@ -445,7 +470,7 @@ def moe_orthogonalize(g, steps=5, out=None, ws=None, stream=None):
     if need == 0:
         raise MoeError(2, "moe_orthogonalize_workspace_size")
     ws = _product_ws(ws, need, index)
-    _launch("moe_orthogonalize", index, stream, g.data_ptr(), _dtype_code(g.dtype), B, M, N, int(steps),
+    _launch("moe_orthogonalize", index, g.data_ptr(), _dtype_code(g.dtype), B, M, N, int(steps),
             out.data_ptr(), ws.data_ptr(), ws.numel())
     return out, ws
 

@@ -5,8 +5,8 @@
 //
 // with 16-bit operands (both bf16 or both fp16) and fp32 accumulators in tensor memory.  The
 // contiguous output dimension is the MMA's M side (operand A), the rows are its N side (operand B),
-// so a ragged last row tile costs its own rows rounded up to 16 instead of a whole tile, and a TMEM
-// lane is an output column: a warp stores 32 neighbouring columns of one row per instruction.
+// so a tile of few rows costs its own rows rounded up to 16 in the MMA instead of a whole tile, and a TMEM
+// lane is an output column.
 // Each operand is K-major (stored [index][k]) or MN-major (stored [k][index]); both come in by TMA
 // with the 128-byte swizzle and only the descriptors differ, so no operand is ever transposed in
 // memory.
@@ -14,7 +14,10 @@
 // One tile is 256 columns x up to 256 rows on a cluster of two CTAs (tcgen05.mma.cta_group::2, M = 256):
 // each CTA loads its own 128 columns and its half of the rows, 32 KB per 64-wide K block for a
 // 128 x 256 x 64 product -- 64 bytes per cycle and SM at the tensor pipe's rate, where a one-CTA tile
-// would need 96.  No load is multicast.
+// would need 96.  No load is multicast.  Tiles of 512 columns, with both accumulators of the tensor memory in
+// one tile and 48 bytes per cycle, were measured and dropped: the accumulators are then not free while the
+// epilogue reads them, and only a contraction of 7000 and more made up for it (K = 8192: 1326 -> 1385
+// TFLOP/s sustained; K = 2880: 1210 -> 1190).
 //
 // Kernel layout (persistent clusters of two, 352 threads per CTA):
 //   warp 0     TMA producer: 6 stages of 32 KB.
@@ -22,14 +25,14 @@
 //   warps 2-9  epilogue: four TMEM lane quarters x two halves of the rows.
 //   warp 10    ragged K: clears the rows behind a segment in its last K block.
 // Tiles are dealt round-robin.  The tiles of the last, partly filled round are split along K when
-// that shortens the round (few rows, one token: split_of); each part stores its fp32 accumulators and
+// that shortens the round (few rows, one token: cost_of); each part stores its fp32 accumulators and
 // the last part to arrive (an atomic counter per warp's share, no waiting) adds them in the order of
 // the parts, so results do not depend on timing.
 //
 // Rounding.  The tensor core truncates when it aligns an addend to its accumulator, which biases a
 // long sum towards zero: about 1e-9 of the sum for every k (measured on this GPU through a library
 // product with fp32 results: 1e-6 at k = 1024, 4.4e-6 at 4096, 1.9e-5 at 16384).  Where the result stays
-// fp32 (PROMOTE), the accumulator is therefore drained every 512 k into registers and added there,
+// fp32 (kPromote), the accumulator is therefore drained every 512 k into registers and added there,
 // rounded to nearest; a 16-bit result, 2^-9 wide, does not see it.
 //
 // Every wait is bounded (kWaitLimitNs); on expiry the kernel sets kErrTimeout and returns.
@@ -90,6 +93,7 @@ constexpr int kMaxParts = 148;           // split tiles x parts
 constexpr int kMaxSplit = 16;
 constexpr size_t kCounterBytes = 8192;   // 16 per split tile; fewer split tiles than clusters (<= 74)
 constexpr size_t kPartialOffset = kWsHeader + kCounterBytes;
+static_assert(kPartialOffset == MOE_PRODUCT_WS_ZEROED, "what has to be zero before the first launch");
 inline int partial_rows(long long rows) { return rows >= kTile ? kTile : (int)((rows + 31) / 32 * 32); }
 inline size_t partial_bytes(int prows) { return (size_t)kMaxParts * 2 * 128 * 4 * (size_t)prows; }
 
@@ -193,7 +197,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
                : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // generic accesses of shared memory before -> the TMA's or the tensor core's after
@@ -398,8 +401,8 @@ __device__ __forceinline__ void store_sector(uint16_t* p, const uint32_t* w) {
 
 // Where the output's rows are the tile's columns (kApply by the choice of operands, the symmetric products by
 // symmetry) a lane's 32 values are 64 contiguous bytes of its own row, and nothing goes through shared
-// memory, whose bandwidth the operands of the MMAs use up: chunks staged there took 10000 to 18000 cycles a
-// tile beside 16400 of MMA (K = 2048).  Pitches are multiples of 16 elements, so whole sectors move, and so
+// memory, which the operands of the MMAs keep busy: with chunks turned there kApply took 420 us on 8 matrices
+// of 2048 x 7168 and 49 on 6 of 2001 x 999, so 378 and 35.  Pitches are multiples of 16 elements, so whole sectors move, and so
 // are the rows of a tile or they end in zeros.
 __device__ __forceinline__ long long lane_row(const Params& p, const Item& x, int rows, int j0, int col) {
   return ((long long)x.g * rows + col) * p.ld + x.r0 + j0;
@@ -822,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int h = (warp - 2) >> 2;  // which half of the tile's rows, in chunks of 32
     uint32_t use = 0;
     bool ok = true;
-uint8_t* const buf0 = staging + (warp - 2) * staging_of(EPI);
+    uint8_t* const buf0 = staging + (warp - 2) * staging_of(EPI);
     uint32_t stored = 0;  // kGrad: chunks stored, alternately from two buffers
     uint32_t next[16];    // the next chunk's addend
     for (int i = cluster_id; i < sc.items && ok; i += n_clusters) {

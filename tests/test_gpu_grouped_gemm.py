@@ -413,3 +413,24 @@ def test_unaligned_and_small_workspaces_are_refused(cuda_device):
     assert ws is not small
     with pytest.raises(ValueError):
         moe.moe_grouped_gemm(x, off, w, ws=torch.zeros(1 << 26, dtype=torch.float32, device="cuda"))
+
+
+def test_what_a_call_allocates_belongs_to_its_stream(cuda_device):
+    """the workspace's zeroing and the output of a call with ``stream`` are ordered on that stream, whatever
+    the current one is busy with"""
+    off = offsets_of([4, 0, 9])
+    x, dy, w = data(17, 13, 3, 1000, 1504, BF)
+    want = moe.moe_grouped_gemm(x, off, w, out_dtype=F32)[0], moe.moe_orthogonalize(w.float())[0]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        torch.cuda._sleep(20_000_000)  # the current stream is behind
+        y, ws = moe.moe_grouped_gemm(x, off, w, out_dtype=F32, stream=side)
+        side.synchronize()
+        assert torch.equal(y, want[0]) and moe.moe_get_device_error(ws, side) == 0
+    wf = w.float()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    u, _ = moe.moe_orthogonalize(wf, stream=side)
+    side.synchronize()
+    assert torch.equal(u, want[1])
