@@ -349,6 +349,7 @@ moe_status_t moe_update_router_bias(const int32_t* counts, int E, float gamma, f
  * fp32 additions in a fixed order.  Results do not depend on timing.  dw is overwritten.
  * N and K are multiples of 8 up to 65536; 1 <= E <= 1024; M >= 0 (M = 0: y / dx empty, dw zeros).
  * Any number of rows per segment; few rows (one token) stream the active experts' weights once.
+ * An output must not overlap an operand.
  *   ws: at least the matching _workspace_size() bytes, the first MOE_PRODUCT_WS_ZEROED of them zero-filled
  *       before its first use (later calls of these entry points and of moe_orthogonalize may share it, one
  *       at a time; zero them again after a MOE_ERR_TIMEOUT); first 256 bytes: the device error word.
