@@ -163,10 +163,11 @@ struct Layout {
   size_t norms, hi0, hi1, lo, gram, poly, total;
 };
 
-// Enough matrices side by side that the launch with the fewest tiles, the Gram matrix's, fills four rounds
-// of 74 clusters, within 1 GB of X.
-constexpr long long kTargetTiles = 296;
-constexpr long long kBatchBytes = 1LL << 30;
+// Enough matrices side by side that the launch with the fewest tiles, the Gram matrix's, fills eight rounds
+// of 74 clusters, within 768 MB of X.  With one round's worth 300 x [128, 128] took 510 us, with four 304, now
+// 216; 8 x [2048, 7168] 4062, 3451 and 3493.
+constexpr long long kTargetTiles = 592;
+constexpr long long kBatchBytes = 3LL << 28;
 
 bool layout_of(int B, int M, int N, Layout& l) {
   if (B <= 0 || M <= 0 || N <= 0 || M > 65536 || N > 65536) return false;
