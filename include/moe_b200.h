@@ -347,7 +347,8 @@ moe_status_t moe_update_router_bias(const int32_t* counts, int E, float gamma, f
  *              they bound are then unspecified).
  * Sums are accumulated in fp32 and rounded once; a sum of a long segment into fp32 is as exact as
  * fp32 additions in a fixed order.  Results do not depend on timing.  dw is overwritten.
- * N and K are multiples of 8 up to 65536; 1 <= E <= 1024; M >= 0 (M = 0: y / dx empty, dw zeros).
+ * N and K are multiples of 8 up to 65536; 1 <= E <= 1024; 0 <= M <= 2^31 - 65536 (M = 0: y / dx empty, dw
+ * zeros); (M / 256 + 1) E (max(N, K) / 256 + 1) < 2^30 with whole quotients.
  * Any number of rows per segment; few rows (one token) stream the active experts' weights once.
  * An output must not overlap an operand.
  *   ws: at least the matching _workspace_size() bytes, the first MOE_PRODUCT_WS_ZEROED of them zero-filled

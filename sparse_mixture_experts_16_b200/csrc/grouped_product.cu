@@ -14,6 +14,9 @@ using namespace moe::product;
 
 namespace {
 
+// rows that can be rounded up to whole tiles, K blocks or means of segments within 32 bits
+constexpr int kMostRows = 0x7fffffff - 65535;
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 moe_status_t shape_status(int M, int E, int N, int K, int dtype) {
@@ -21,7 +24,9 @@ moe_status_t shape_status(int M, int E, int N, int K, int dtype) {
   if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP16) return MOE_ERR_INVALID_ARG;
   // rows of 16-bit elements that TMA can step over, and coordinates and tile counts within 32 bits
   if (N % 8 != 0 || K % 8 != 0 || N > 65536 || K > 65536 || E > kMaxGroups) return MOE_ERR_UNSUPPORTED_SHAPE;
-  const long long tiles = ((long long)M / kTile + E) * ((N > K ? N : K) / kTile + 1);
+  if (M > kMostRows) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // whatever the offsets are: clamped, each segment has at most M rows
+  const long long tiles = ((long long)M / kTile + 1) * E * ((N > K ? N : K) / kTile + 1);
   if (tiles >= (1LL << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
 }

@@ -89,6 +89,19 @@ def test_orthogonalize_workspace(L):
     assert size(1, 2048, 7168) < size(2, 2048, 7168)
 
 
+@pytest.mark.parametrize("M,E,status", [
+    (2**31 - 65535, 1, 2), (2**31 - 1, 8, 2),   # rounding up to tiles would pass 32 bits
+    (2**30, 1024, 2),                           # offsets 0, M, 0, M, ... would make 2^31 tiles
+    (2**31 - 65536, 1, 3), (2**28 - 256, 1023, 3),  # large enough: the next check, alignment, refuses these
+])
+def test_products_refuse_rows_past_32_bits(L, M, E, status):
+    need = L.moe_grouped_gemm_workspace_size(M)
+    for name in ("moe_grouped_gemm", "moe_grouped_gemm_dgrad"):
+        assert _rows(L, name, M=M, E=E, N=8, K=8, x=X + 8, ws_bytes=need) == status
+    need = L.moe_grouped_gemm_wgrad_workspace_size(8)
+    assert L.moe_grouped_gemm_wgrad(X + 8, W, OFF, M, E, 8, 8, 0, OUT, WS, need, None) == status
+
+
 def test_python_refuses_host_tensors_and_wrong_types():
     x = torch.zeros(4, 16, dtype=torch.bfloat16)
     w = torch.zeros(2, 8, 16, dtype=torch.bfloat16)
