@@ -580,6 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail_bar + kStages);
   uint8_t* staging = smem + kStages * kStageBytes + kBarBytes;
   int* sched_smem = reinterpret_cast<int*>(staging + kEpiWarps * staging_of(EPI));
+  volatile uint32_t* progress = reinterpret_cast<uint32_t*>(sched_smem + 3);  // kRaggedK: see the tail blocks
   int* tab = sched_smem + 4;  // item_of's table
 
   // the parameters' lines are fetched while the barriers are set up, not one by one where they are used
@@ -590,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   const int cluster_id = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
 
   if (warp == 0 && lane == 0) {
+    if (RAGGED == kRaggedK) *progress = 0;
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], RAGGED == kRaggedK ? 2 : 1);  // kRaggedK: see the tail blocks below
       mbar_init(&empty[s], 1);
@@ -687,6 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             ok = false;
             break;
           }
+          if (RAGGED == kRaggedK && (it & 0xffff) == 0) *progress = it;
           uint8_t* sa = smem + stage * kStageBytes;
           uint8_t* sb = sa + kTileA;
           const int kx = kb * kBK;
@@ -791,7 +794,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     // at r * 128 (the swizzle permutes within a row), so once the block has landed its rows up to the
     // next multiple of 16 are zeroed in both operands and the stage is handed to the MMA; the producer
     // has gone on meanwhile.  Of the full barrier's two arrivals each CTA makes one here; for the other
-    // blocks the even CTA's producer makes both, so that no arrival crosses the pair.
+    // blocks the even CTA's producer makes both, so that no arrival crosses the pair.  A tile of a segment
+    // of 10^8 rows can take longer than one wait may, so a wait that has expired is made again if the
+    // producer has come on by 2^16 blocks (some 30 ms) in it.
     if constexpr (RAGGED == kRaggedK) {
       uint32_t it = 0, phases = 0;
       bool ok = true;
@@ -801,7 +806,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         it += count;
         if (count <= 0 || !ragged_tail(x.krows, kx)) continue;
         const int stage = (it - 1) % kStages;
-        ok = __all_sync(0xffffffffu, sleep_wait(&tail_bar[stage], (phases >> stage) & 1));
+        uint32_t seen = *progress;
+        while (!(ok = __all_sync(0xffffffffu, sleep_wait(&tail_bar[stage], (phases >> stage) & 1)))) {
+          const uint32_t now = __shfl_sync(0xffffffffu, *progress, 0);
+          if (__shfl_sync(0xffffffffu, seen, 0) == now) break;
+          seen = now;
+        }
         phases ^= 1u << stage;
         if (!ok) break;
         uint8_t* sa = smem + stage * kStageBytes;

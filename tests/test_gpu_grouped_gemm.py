@@ -363,6 +363,23 @@ def test_outputs_past_32_bits(cuda_device):
         close(dw[e], a @ b, a.abs() @ b.abs(), 2)
 
 
+def test_a_segment_that_takes_longer_than_a_wait(cuda_device):
+    """2^29 + 3 rows in one of 100 segments, whose tile is not split: the wait for its last block would expire.
+    The products are -1, 0 or 1 and their sums stay far below 2^24, so that every order of adding is exact."""
+    E, M, N, K = 100, 2 ** 29 + 3, 8, 8
+    g = torch.Generator(device="cuda").manual_seed(11)
+    x = torch.empty(M, K, dtype=BF, device="cuda").random_(-1, 2, generator=g)
+    dy = torch.empty(M, N, dtype=BF, device="cuda").random_(-1, 2, generator=g)
+    off = offsets_of([M] + [0] * (E - 1))
+    dw, ws = moe.moe_grouped_gemm_wgrad(dy, x, off)
+    assert moe.moe_get_device_error(ws) == 0
+    ref = torch.zeros(N, K, dtype=torch.float64, device="cuda")
+    for at in range(0, M, 2 ** 24):
+        ref += dy[at:at + 2 ** 24].double().T @ x[at:at + 2 ** 24].double()
+    assert ref.abs().max() < 2 ** 24
+    assert torch.equal(dw[0].double(), ref) and not dw[1:].any()
+
+
 def test_two_streams_with_a_workspace_each(cuda_device):
     """calls that run side by side, each on its own stream and workspace, give what they give alone"""
     off = offsets_of([100, 3, 0, 500])
