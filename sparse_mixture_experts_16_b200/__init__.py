@@ -349,7 +349,7 @@ def _on_stream(function):
             return function(*args, **kwargs)
         import torch
 
-        device = (args[0] if args else next(iter(kwargs.values()))).device
+        device = next(a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor)).device
         if device != stream.device:
             raise ValueError(f"stream: expected a stream on {device}, got {stream.device}")
         with torch.cuda.stream(stream):

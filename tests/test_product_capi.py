@@ -118,3 +118,12 @@ def test_python_refuses_host_tensors_and_wrong_types():
         moe.moe_orthogonalize(torch.zeros(4, 4))
     with pytest.raises(ValueError):
         moe.moe_orthogonalize(torch.zeros(4, 4, dtype=torch.float64))
+
+
+def test_python_finds_the_operands_device_among_keywords():
+    class Stream:
+        device = torch.device("cuda", 0)
+
+    for kwargs in (dict(steps=5, g=torch.zeros(4, 4)), dict(out=None, g=torch.zeros(4, 4))):
+        with pytest.raises(ValueError, match="expected a stream on cpu"):
+            moe.moe_orthogonalize(**kwargs, stream=Stream())
