@@ -322,6 +322,12 @@ def _need_at(t, dtype, shape, index, name):
     raise ValueError(f"{name}: expected a tensor on cuda:{index}, got {t.device}")
 
 
+def _need_int32(name, *sizes):
+    """sizes that the C entry point can be given: ctypes would drop their upper bits"""
+    if max(sizes) > 0x7FFFFFFF:
+        raise MoeError(2, name)
+
+
 @functools.lru_cache(maxsize=4096)
 def _ws_size(name, *sizes):
     return getattr(lib(), name)(*sizes)
@@ -384,6 +390,7 @@ def _rows_product(name, rows, offsets, w, contracted, wide, out, out_dtype, ws):
     sizes = w.shape
     E, N, K = sizes
     M = rows.shape[0]
+    _need_int32(name, M, E, N, K)
     index = rows.get_device()
     _need_at(rows, dtype, (M, sizes[contracted]), index, "x" if contracted == 2 else "dy")
     _need_at(w, dtype, sizes, index, "w")
@@ -430,6 +437,7 @@ def moe_grouped_gemm_wgrad(dy, x, offsets, out=None, ws=None):
         raise ValueError("expected dy [M, N], x [M, K] and offsets [E+1]")
     M, N = dy.shape
     K, E = x.shape[1], offsets.numel() - 1
+    _need_int32("moe_grouped_gemm_wgrad", M, E, N, K)
     index = dy.get_device()
     _need_at(dy, dtype, (M, N), index, "dy")
     _need_at(x, dtype, (M, K), index, "x")
@@ -456,14 +464,15 @@ def moe_orthogonalize(g, steps=5, out=None, ws=None):
         raise ValueError(f"g: expected float32 or bfloat16, got {g.dtype}")
     if g.dim() < 2:
         raise ValueError("g: expected [..., M, N]")
+    M, N = g.shape[-2:]
+    B = g.numel() // (M * N) if M * N else 0
+    _need_int32("moe_orthogonalize", B, M, N)
     index = g.get_device()
     _need_at(g, g.dtype, g.shape, index, "g")
-    M, N = g.shape[-2:]
     if out is None:
         out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
     else:
         _need_at(out, torch.bfloat16, g.shape, index, "out")
-    B = g.numel() // (M * N) if M * N else 0
     if B == 0:
         return out, ws
     need = _ws_size("moe_orthogonalize_workspace_size", B, M, N)

@@ -127,3 +127,16 @@ def test_python_finds_the_operands_device_among_keywords():
     for kwargs in (dict(steps=5, g=torch.zeros(4, 4)), dict(out=None, g=torch.zeros(4, 4))):
         with pytest.raises(ValueError, match="expected a stream on cpu"):
             moe.moe_orthogonalize(**kwargs, stream=Stream())
+
+
+def test_python_refuses_sizes_past_32_bits():
+    big = 2 ** 32 + 8  # its lower 32 bits would be a valid size
+    rows = torch.zeros(1, 8, dtype=torch.bfloat16).expand(big, 8)
+    w = torch.zeros(2, 8, 8, dtype=torch.bfloat16)
+    off = torch.zeros(3, dtype=torch.int32)
+    for call in (lambda: moe.moe_grouped_gemm(rows, off, w), lambda: moe.moe_grouped_gemm_dgrad(rows, off, w),
+                 lambda: moe.moe_grouped_gemm_wgrad(rows, rows, off),
+                 lambda: moe.moe_orthogonalize(torch.zeros(1, 1, 1).expand(big, 1, 1)),
+                 lambda: moe.moe_orthogonalize(torch.zeros(1, 1).expand(2, big))):
+        with pytest.raises(moe.MoeError, match="UNSUPPORTED_SHAPE"):
+            call()
