@@ -379,9 +379,11 @@ moe_status_t moe_grouped_gemm_wgrad(const void* dy, const void* x, const int32_t
  *   g    [B, M, N]  fp32 or bf16 (g_dtype), e.g. dw of moe_grouped_gemm_wgrad, or dgate_up of
  *                   moe_layer_backward seen as [2E, F, D]
  *   out  [B, M, N]  bf16 (must not overlap g)
- * Computed in fp16 with a low-order part of X and fp32 accumulation, or in fp32 where the shorter side is
- * at most 64; the result is rounded to bf16 once, and after up to 5 steps it is within bf16's rounding of
- * the exact iterate in the 2-norm.  Each further step multiplies what rounding has added in directions that
+ * Computed in fp16 with a low-order part of X, an fp32 diagonal of the polynomial and fp32 accumulation, or in
+ * fp32 where the shorter side is at most 64; the result is rounded to bf16 once (1.7e-3 of its Frobenius norm).
+ * After up to 5 steps the iterate before that rounding is off by at most 1e-3 of the Frobenius norm for a matrix of
+ * a few directions (rank 1 to 8, one over a faint rest) and 1.5e-3 for other spectra, diagonal matrices 3e-3
+ * (simulated roundings).  Each further step multiplies what rounding has added in directions that
  * the matrix hardly has by up to a.  A matrix that holds a NaN or an infinity comes out as NaN; the others
  * of the batch are not affected.  Any sizes 1 <= M, N <= 65536, odd ones too; B >= 0; 1 <= steps <= 16 (5 is
  * usual).

@@ -14,16 +14,20 @@
 // 3 m^2 n + m^3 products per step for n = max(M, N), a quarter to a third below the plain form's.
 //
 // Numerics.  Operands are fp16 scaled by 2^12 (not bf16: the same tensor-core rate with 1/8 of the
-// rounding; |X| <= 1.2025, |A| <= 1.45, |P| <= 3.4445, so nothing overflows, and values down to 2^-36
+// rounding; |X| <= 1.2025, |A| <= 1.45, |P - a I| <= 2.81, so nothing overflows, and values down to 2^-36
 // keep a bit).  A singular value v grows by up to a^steps = 485, and so does what rounding adds along
-// directions that the matrix does not have; gradients of experts with few tokens are of such low
-// rank.  X is therefore kept as hi + lo * 2^-11 (22 bits): the tensor core multiplies hi, and
-// a lo * 2^-11 is added to the product.  The last step multiplies hi alone: what it leaves out grows
-// by a once.  In a simulation of exactly these roundings over nine spectra (full rank, rank 8 and 64,
-// polynomial and geometric decay, one huge entry) the result is 4e-4 to 1.7e-3 off in the 2-norm, no
-// more than its rounding to bf16; without lo 4e-2, without lo in the last two steps 2.9e-3, with bf16
-// operands 3e-1 (rank 8).  P uses the rounded A in both terms: its error is then that of a nearby X,
-// which the iteration damps (with the unrounded A in b A it is twice as large).
+// directions that the matrix does not have; gradients of experts with few tokens are of such low rank.
+// Two roundings would do that, and are not made:
+//   X is kept as hi + lo * 2^-11 (22 bits): the tensor core multiplies hi, and a lo * 2^-11 is added.
+//   P's diagonal, which a I makes larger than all the rest, stays in fp32 beside it (the fp16 P has zeros
+//   there) and multiplies hi in the epilogue; lo meets a alone, for the rest of P has not met it either.
+// In a simulation of exactly these roundings over thirteen spectra, 65 x 3000 to 384 x 768, the last iterate is
+// off by at most this share of its Frobenius norm, before its rounding to bf16 takes another 1.7e-3: rank 1, 4
+// and 8 and one value over a tail of 1e-5 6e-4 to 8e-4, full rank, rank 64, polynomial and geometric decay and one huge
+// entry 4e-4 to 1.4e-3, a diagonal matrix with geometric decay 2.9e-3 (A's own rounding).  With a I inside the
+// fp16 P rank 1 and the tail are 2.4e-3 off, without lo 4e-2, with bf16 operands 3e-1 (rank 8).  P uses
+// the rounded A in both terms: its error is then that of a nearby X, which the iteration damps (with the unrounded
+// A in b A it is twice as large).
 // The norm is summed in 64 bits, so fp32 inputs of any magnitude neither overflow nor vanish.
 #include "product_sm100.cuh"
 
@@ -160,7 +164,7 @@ struct Layout {
   int low, lp, np;   // shorter side, its pitch, the pitch of X's rows
   int batch;         // matrices per round of launches
   int prows;
-  size_t norms, hi0, hi1, lo, gram, poly, total;
+  size_t norms, hi0, hi1, lo, gram, poly, diag, total;
 };
 
 // Enough matrices side by side that the launch with the fewest tiles, the Gram matrix's, fills eight rounds
@@ -193,6 +197,7 @@ bool layout_of(int B, int M, int N, Layout& l) {
   l.lo = take(x);
   l.gram = take(s);
   l.poly = take(s);
+  l.diag = take((size_t)l.batch * l.lp * sizeof(float));
   l.total = at;
   return true;
 }
@@ -225,6 +230,8 @@ cudaError_t iterate(int count, int M, int N, int steps, const Layout& l, uint16_
   uint16_t* hi[2] = {reinterpret_cast<uint16_t*>(b + l.hi0), reinterpret_cast<uint16_t*>(b + l.hi1)};
   uint16_t* gram = reinterpret_cast<uint16_t*>(b + l.gram);
   uint16_t* poly = reinterpret_cast<uint16_t*>(b + l.poly);
+  base.diag = reinterpret_cast<float*>(b + l.diag);
+  base.diag_ld = l.lp;
   const OperandHost og = {gram, (uint64_t)l.lp, (uint64_t)l.low, G};
   const OperandHost op = {poly, (uint64_t)l.lp, (uint64_t)l.low, G};
   for (int k = 0; k < steps; ++k) {
@@ -260,41 +267,29 @@ cudaError_t iterate(int count, int M, int N, int steps, const Layout& l, uint16_
     p.src = gram;
     p.c0 = kNsB;
     p.c1 = kNsC * kUnscale;
-    p.c2 = kNsA * kScale;
+    p.c2 = kNsA;
     if (!set_operands<false, false>(p, og, og, false)) return cudaErrorInvalidValue;
     if ((e = launch<false, false, kDense, kPoly>(p, s)) != cudaSuccess) return e;
 
     p = base;
     p.K = l.lp;
     p.kb_typ = (p.K + kBK - 1) / kBK;
-    if (last) {
-      p.rows = p.rows_typ = M;
-      p.cols = l.np;
-      p.cols_out = N;
-      p.out = out;
-      p.c1 = kUnscale * kUnscale;
-      if (tall) {  // X P: P's rows are the columns, X's rows the rows
-        if (!set_operands<false, false>(p, op, ox, false)) return cudaErrorInvalidValue;
-        e = launch<false, false, kDense, kApplyLast>(p, s);
-      } else {     // P X: X is contracted over its rows
-        if (!set_operands<true, false>(p, ox, op, false)) return cudaErrorInvalidValue;
-        e = launch<true, false, kDense, kApplyLast>(p, s);
-      }
-    } else {       // the same with rows and columns exchanged
-      p.rows = p.rows_typ = p.ld = l.np;
-      p.cols = M;
-      p.src = lo;
-      p.out = hi[(k + 1) & 1];
-      p.out_lo = k < steps - 2 ? lo : nullptr;
-      p.c0 = kNsA / 2048.0f;
-      p.c1 = kUnscale;
-      if (tall) {
-        if (!set_operands<false, false>(p, ox, op, false)) return cudaErrorInvalidValue;
-        e = launch<false, false, kDense, kApply>(p, s);
-      } else {
-        if (!set_operands<false, true>(p, op, ox, false)) return cudaErrorInvalidValue;
-        e = launch<false, true, kDense, kApply>(p, s);
-      }
+    p.rows = p.rows_typ = p.ld = l.np;  // the product's rows and columns are exchanged
+    p.cols = M;
+    p.cols_out = N;
+    p.src = hi[k & 1];
+    p.src_lo = lo;
+    p.out = last ? out : hi[(k + 1) & 1];
+    p.out_lo = lo;
+    p.c0 = kUnscale;
+    p.c1 = kUnscale;
+    p.c2 = kNsA / 2048.0f;
+    if (tall) {  // X P
+      if (!set_operands<false, false>(p, ox, op, false)) return cudaErrorInvalidValue;
+      e = last ? launch<false, false, kDense, kApplyLast>(p, s) : launch<false, false, kDense, kApply>(p, s);
+    } else {     // P X: X is contracted over its rows
+      if (!set_operands<false, true>(p, op, ox, false)) return cudaErrorInvalidValue;
+      e = last ? launch<false, true, kDense, kApplyLast>(p, s) : launch<false, true, kDense, kApply>(p, s);
     }
     if (e != cudaSuccess) return e;
   }

@@ -58,9 +58,11 @@ enum Epilogue {
   kOut16 = 0,     // out = bf16 or fp16
   kOut32 = 1,     // out = fp32, promoted accumulation
   kGram = 2,      // symmetric: out = fp16(acc * c1), and its mirror image
-  kPoly = 3,      // symmetric: out = fp16(c0 * src + acc * c1), c2 added on the diagonal, and its mirror image
-  kApply = 4,     // x = acc * c1 + src * c0; out = fp16(x), out_lo = fp16(2048 (x - out)): out[column][row]
-  kApplyLast = 5, // out = bf16(acc * c1), rows of cols_out elements
+  kPoly = 3,      // symmetric: out = fp16(c0 * src + acc * c1), and its mirror image; the diagonal goes to diag as
+                  // c2 + diagonal / 4096, and out has zeros there
+  kApply = 4,     // x = acc * c1 + diag * src + c2 * src_lo; out = fp16(x), out_lo = fp16(2048 (x - out)):
+                  // out[column][row]
+  kApplyLast = 5, // out = bf16(the same x * c0), rows of cols_out elements: out[column][row]
   kGrad = 6       // as kOut32, of groups of equal rows: leaves by TMA
 };
 
@@ -79,6 +81,7 @@ constexpr int kChunkBytes = 32 * 32 * 2;  // 32 rows x 32 columns of 16 bits: wh
 // shared memory of an epilogue warp: a chunk of 16 bits turned from columns to rows; kGrad: two chunks of fp32
 // on their way out
 constexpr int staging_of(int epi) { return epi == kGrad ? 4 * kChunkBytes : epi == kOut32 || epi == kApply ? 0 : kChunkBytes; }
+constexpr bool applies(int epi) { return epi == kApply || epi == kApplyLast; }
 constexpr int stages_of(int epi) { return epi == kGrad ? kStages - 1 : kStages; }
 // groups whose segments' bounds are held in shared memory (kGrad: what the staging leaves room for)
 constexpr int table_groups(int epi) { return epi == kGrad ? 190 : kMaxGroups; }
@@ -118,10 +121,13 @@ struct alignas(64) Params {
   uint32_t idesc;          // instruction descriptor without M and N
   int out_bf16;            // kOut16: bf16 instead of fp16
   int ld;                  // row pitch of src, src_lo, out, out_lo of the Newton-Schulz epilogues
-  int cols_out;            // kApplyLast: row pitch of out, columns that are stored
+  int cols_out;            // kApply, kApplyLast: columns of a row of X that exist; the latter: row pitch of out
   void* out;
-  uint16_t* out_lo;        // kApply; null: not kept
-  const uint16_t* src;     // kPoly: symmetric; kApply: of out's layout, may be out_lo
+  uint16_t* out_lo;        // kApply
+  const uint16_t* src;     // kPoly: symmetric; kApply, kApplyLast: X's high-order part
+  const uint16_t* src_lo;  // kApply, kApplyLast: its low-order part, may be out_lo
+  float* diag;             // kPoly: written, kApply and kApplyLast: read; a group's stands at its number x diag_ld
+  int diag_ld;
   float c0, c1, c2;
   float* partial;
   int* counters;
@@ -412,14 +418,31 @@ __device__ __forceinline__ void store_lane_row(uint16_t* o, const uint32_t (&w)[
   if (nj > 16) store_sector(o + 16, w + 8);
 }
 
-// what kPoly and kApply add to a chunk: read one chunk ahead
+// what kPoly, kApply and kApplyLast add to a chunk: read one chunk ahead
 template <int EPI>
-__device__ __forceinline__ void load_addend(const Params& p, const Item& x, uint32_t (&s)[16], int j0, int col) {
+struct Addend {
+  uint32_t hi[16];
+  uint32_t lo[applies(EPI) ? 16 : 1];
+  float diag;  // P X: of this lane's row of X; X P: of column j0 + lane of X
+};
+template <int EPI, bool PX>
+__device__ __forceinline__ void load_addend(const Params& p, const Item& x, Addend<EPI>& s, int j0, int col, int lane) {
   const int rows = EPI == kPoly ? p.rows : p.cols;
-  if (j0 >= x.nr || col >= rows) return;
-  const uint16_t* at = p.src + lane_row(p, x, rows, j0, col);
-  load_sector(at, s);
-  if (x.nr - j0 > 16) load_sector(at + 16, s + 8);
+  if (j0 >= x.nr) return;
+  const bool two = x.nr - j0 > 16;
+  if (col < rows) {
+    const long long at = lane_row(p, x, rows, j0, col);
+    load_sector(p.src + at, s.hi);
+    if (two) load_sector(p.src + at + 16, s.hi + 8);
+    if constexpr (applies(EPI)) {
+      load_sector(p.src_lo + at, s.lo);
+      if (two) load_sector(p.src_lo + at + 16, s.lo + 8);
+    }
+  }
+  if constexpr (applies(EPI)) {
+    const int i = PX ? col : x.r0 + j0 + lane;
+    s.diag = i < (PX ? p.cols : p.cols_out) ? __ldcg(p.diag + (long long)x.g * p.diag_ld + i) : 0.0f;
+  }
 }
 
 // A warp's 16-bit chunk, w[i] = rows 2 i and 2 i + 1 of this lane's column, turned through shared memory and
@@ -450,11 +473,41 @@ __device__ __forceinline__ void store_turned(uint16_t* o, int pitch, uint8_t* bu
   __syncwarp();  // the buffer is written again
 }
 
+// A warp's chunk of kApplyLast, w[i] = elements j0 + 2 i and + 1 of row col of X (this lane's), turned through
+// shared memory (16 bytes at a time, permuted within a row so that no two lanes meet in a bank) so that a
+// row's 64 bytes lie side by side in a store.  Of another pitch than whole 16 bytes, a row at a time.
+__device__ __forceinline__ void store_rows(const Params& p, const Item& x, uint8_t* buf, const uint32_t (&w)[16], int j0,
+                                           int nj, int col, int lane) {
+  const int pitch = p.cols_out, c0 = x.r0 + j0;
+  const int limit = min(nj, pitch - c0), rows = min(32, p.cols - (col - lane));  // that exist
+  uint16_t* o = static_cast<uint16_t*>(p.out) + ((long long)x.g * p.cols + col - lane) * pitch + c0;
+  uint4* b = reinterpret_cast<uint4*>(buf);
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    b[lane * 4 + (u ^ ((lane >> 1) & 3))] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+  __syncwarp();
+  if ((pitch & 7) == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (lane >> 2) + 8 * i, u = lane & 3;
+      const uint4 v = b[r * 4 + (u ^ ((r >> 1) & 3))];
+      if (r < rows && 8 * u < limit) *reinterpret_cast<uint4*>(o + (long long)r * pitch + 8 * u) = v;
+    }
+  } else {
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      const uint16_t v = reinterpret_cast<const uint16_t*>(b)[r * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) * 8) + (lane & 7)];
+      if (r < rows && lane < limit) o[(long long)r * pitch + lane] = v;
+    }
+  }
+  __syncwarp();  // the buffer is written again
+}
+
 // One warp's 32 rows x 32 columns, v[j] = accumulator of row j0 + j and column col (this lane's), s its
-// addend; nj rows are valid.
-template <int RAGGED, int EPI>
+// addend; nj rows are valid.  PX: X is multiplied from the left.
+template <int RAGGED, int EPI, bool PX>
 __device__ __forceinline__ void emit(const Params& p, const Item& x, uint8_t* buf, const float (&v)[32],
-                                     const uint32_t (&s)[16], int j0, int nj, int col, int lane) {
+                                     const Addend<EPI>& s, int j0, int nj, int col, int lane) {
   const int row_in = x.r0 + j0;  // row within the group
   const long long row = (RAGGED == kRaggedRows ? (long long)x.row0 : (long long)x.g * p.rows) + row_in;
   uint16_t* const out = static_cast<uint16_t*>(p.out);
@@ -469,33 +522,46 @@ __device__ __forceinline__ void emit(const Params& p, const Item& x, uint8_t* bu
       for (int j = 0; j < 32; ++j)
         if (j < nj) o[(long long)j * p.cols] = v[j];
     }
-  } else if constexpr (EPI == kApply) {
-    if (col >= p.cols) return;
+  } else if constexpr (applies(EPI)) {
     uint32_t hi[16], lo[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {  // two at a time: only the conversions of pairs run at full rate
-      const float2 a = unpack_half(s[i]);
-      const float w0 = v[2 * i] * p.c1 + a.x * p.c0, w1 = v[2 * i + 1] * p.c1 + a.y * p.c0;
-      hi[i] = pack_half(w0, w1);
-      const float2 f = unpack_half(hi[i]);
-      lo[i] = pack_half((w0 - f.x) * 2048.0f, (w1 - f.y) * 2048.0f);
+      const float2 a = unpack_half(s.hi[i]), b = unpack_half(s.lo[i]);
+      const float d0 = PX ? s.diag : __shfl_sync(0xffffffffu, s.diag, 2 * i);
+      const float d1 = PX ? s.diag : __shfl_sync(0xffffffffu, s.diag, 2 * i + 1);
+      const float w0 = v[2 * i] * p.c1 + d0 * a.x + p.c2 * b.x;
+      const float w1 = v[2 * i + 1] * p.c1 + d1 * a.y + p.c2 * b.y;
+      if constexpr (EPI == kApplyLast) {
+        hi[i] = pack_bf16(w0 * p.c0, w1 * p.c0);
+      } else {
+        hi[i] = pack_half(w0, w1);
+        const float2 f = unpack_half(hi[i]);
+        lo[i] = pack_half((w0 - f.x) * 2048.0f, (w1 - f.y) * 2048.0f);
+      }
     }
-    const long long at = lane_row(p, x, p.cols, j0, col);
-    store_lane_row(out + at, hi, nj);
-    if (p.out_lo != nullptr) store_lane_row(p.out_lo + at, lo, nj);
+    if constexpr (EPI == kApplyLast) {
+      store_rows(p, x, buf, hi, j0, nj, col, lane);
+    } else if (col < p.cols) {
+      const long long at = lane_row(p, x, p.cols, j0, col);
+      store_lane_row(out + at, hi, nj);
+      store_lane_row(p.out_lo + at, lo, nj);
+    }
   } else {
     uint32_t w[16];
     if constexpr (EPI == kPoly) {
+      const int at = col - row_in;  // the row of the diagonal's element
+      float d = 0.0f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float2 a = unpack_half(s[i]);
-        w[i] = pack_half(v[2 * i] * p.c1 + a.x * p.c0 + (row_in + 2 * i == col ? p.c2 : 0.0f),
-                         v[2 * i + 1] * p.c1 + a.y * p.c0 + (row_in + 2 * i + 1 == col ? p.c2 : 0.0f));
+        const float2 a = unpack_half(s.hi[i]);
+        const float w0 = v[2 * i] * p.c1 + a.x * p.c0, w1 = v[2 * i + 1] * p.c1 + a.y * p.c0;
+        d = at == 2 * i ? w0 : at == 2 * i + 1 ? w1 : d;
+        w[i] = pack_half(at == 2 * i ? 0.0f : w0, at == 2 * i + 1 ? 0.0f : w1);
       }
-    } else if (EPI == kApplyLast || (EPI == kOut16 && p.out_bf16)) {
-      const float c = EPI == kApplyLast ? p.c1 : 1.0f;
+      if (at >= 0 && at < nj && col < p.rows) p.diag[(long long)x.g * p.diag_ld + col] = p.c2 + d * (1.0f / 4096.0f);
+    } else if (EPI == kOut16 && p.out_bf16) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i] * c, v[2 * i + 1] * c);
+      for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     } else {
       const float c = EPI == kGram ? p.c1 : 1.0f;
 #pragma unroll
@@ -505,15 +571,7 @@ __device__ __forceinline__ void emit(const Params& p, const Item& x, uint8_t* bu
       if (col < p.rows) store_lane_row(out + lane_row(p, x, p.rows, j0, col), w, nj);
       if (x.triangle && x.rt != x.ct) store_turned(out + row * p.ld + col - lane, p.ld, buf, w, nj, p.ld - (col - lane), lane);
     } else {
-      const int pitch = EPI == kOut16 ? p.cols : p.cols_out, limit = pitch - (col - lane);
-      uint16_t* o = out + row * pitch + col - lane;
-      if (EPI == kOut16 || (pitch & 7) == 0) {
-        store_turned(o, pitch, buf, w, nj, limit, lane);
-      } else if (lane < limit) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j < nj) o[(long long)j * pitch + lane] = (uint16_t)(w[j / 2] >> 16 * (j & 1));
-      }
+      store_turned(out + row * p.cols + col - lane, p.cols, buf, w, nj, p.cols - (col - lane), lane);
     }
   }
 }
@@ -568,7 +626,8 @@ __device__ __forceinline__ float* part_ptr(const Params& p, int slot, int split,
 // ------------------------------------------------------------------------------ the kernel
 template <bool A_MN, bool B_MN, int RAGGED, int EPI>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p) {
-  constexpr bool kPromote = EPI == kOut32 || EPI == kGrad, kAdds = EPI == kPoly || EPI == kApply;
+  constexpr bool kPromote = EPI == kOut32 || EPI == kGrad, kAdds = EPI == kPoly || applies(EPI);
+  constexpr bool kPX = B_MN;  // kApply, kApplyLast: X is the MN-major operand where it is contracted over its rows
   constexpr int kStages = stages_of(EPI);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -837,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     bool ok = true;
     uint8_t* const buf0 = staging + (warp - 2) * staging_of(EPI);
     uint32_t stored = 0;  // kGrad: chunks stored, alternately from two buffers
-    uint32_t next[16];    // the next chunk's addend
+    Addend<EPI> next;     // the next chunk's addend
     for (int i = cluster_id; i < sc.items && ok; i += n_clusters) {
       const Item x = item_of<RAGGED, EPI>(p, tab, sc, i);
       if (RAGGED == kDense && i == cluster_id) pdl_wait();
@@ -860,13 +919,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         } else if constexpr (EPI == kGrad) {
           emit_grad(p, x, buf0, stored, v, j0, nj, col, lane);
         } else if constexpr (kAdds) {
-          uint32_t s[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) s[j] = next[j];
-          load_addend<EPI>(p, x, next, c + 1 < chunks ? j0 + 32 : x.nr, col);
-          emit<RAGGED, EPI>(p, x, buf0, v, s, j0, nj, col, lane);
+          const Addend<EPI> s = next;
+          load_addend<EPI, kPX>(p, x, next, c + 1 < chunks ? j0 + 32 : x.nr, col, lane);
+          emit<RAGGED, EPI, kPX>(p, x, buf0, v, s, j0, nj, col, lane);
         } else {
-          emit<RAGGED, EPI>(p, x, buf0, v, next, j0, nj, col, lane);
+          emit<RAGGED, EPI, kPX>(p, x, buf0, v, next, j0, nj, col, lane);
         }
       };
       if (kPromote && x.kb1 - x.kb0 > kPromoteBlocks) {
@@ -907,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       } else {
         const uint32_t buf = use & 1;
         if constexpr (kAdds)
-          if (!split && chunks > 0) load_addend<EPI>(p, x, next, first * 32, col);
+          if (!split && chunks > 0) load_addend<EPI, kPX>(p, x, next, first * 32, col, lane);
         ok = __all_sync(0xffffffffu, sleep_wait(&acc_full[buf], (use >> 1) & 1));
         if (!ok) {
           if (lane == 0) set_error(p.err, kErrTimeout);
@@ -950,14 +1007,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           for (int c = 0; c < chunks; ++c) {
             const int j0 = (first + c) * 32;
             const int nj = min(32, x.nr - j0);
-            if constexpr (kAdds) load_addend<EPI>(p, x, next, j0, col);
+            if constexpr (kAdds) load_addend<EPI, kPX>(p, x, next, j0, col, lane);
             const float* part0 = part_ptr(p, x.slot, sc.split, 0, (int)rank) + (size_t)j0 * 128 + q * 32 + lane;
             const size_t pitch = 2 * (size_t)p.prows * 128;
             float v[32];
             if (nj <= 4) add_parts<4, 16>(part0, pitch, sc.split, nj, v);
             else add_parts<8, 8>(part0, pitch, sc.split, nj, v);
             if constexpr (EPI == kGrad) emit_grad(p, x, buf0, stored, v, j0, nj, col, lane);
-            else emit<RAGGED, EPI>(p, x, buf0, v, next, j0, nj, col, lane);
+            else emit<RAGGED, EPI, kPX>(p, x, buf0, v, next, j0, nj, col, lane);
           }
         }
       }
