@@ -11,10 +11,13 @@
 // Numerics, fp32 (FFMA).  The matrices commute only up to rounding: where A has no component a rounding grows
 // by a = 3.4445 per step and side, so the order of the factors matters.  A stays P A P (P (P A) grows by
 // a^2 on one side), and only the symmetric A and P are read by rows in the place of columns: with Q read
-// so, the result is up to 0.4 off.  In simulation the result is at most 1e-3 off after five steps (2 x 2
-// to 64 x 900, rank 4, polynomial and geometric decay), but after sixteen it has diverged.  More than five
-// steps are therefore made in rounds of five, each from the Gram matrix of the X that the last one left in
-// fp32: X is bounded.
+// so, the result is up to 0.4 off.  What rounds A_0 itself grows likewise, and one fp32 chain over a long side
+// rounds it with every term: 4e-3 (8 x 900) to 1.2e-2 (16 x 7168) off, one direction and 1e-2 or 1e-3 of noise.  Its sums
+// are therefore drained every 64 terms into 64 bits, over the parts too, and rounded to fp32 at the end of a part and of
+// all.  In simulation the result is then at most 1e-3 off after five steps, whatever the length and the number of
+// parts (2 x 2 to 64 x 900, rank 4, polynomial and geometric decay; one direction and noise to 8 x 65536: 5.4e-4), but
+// after sixteen it has diverged.  More than five steps are therefore made in rounds of five, each from the Gram
+// matrix of the X that the last one left in fp32: X is bounded.
 //
 // Included by orthogonalize.cu, whose norm partials it uses.
 #pragma once
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(kSmallThreads) small_gram_kernel(const T* __re
   __syncthreads();
   const float2 f = scale;
   const T* m = g + (long long)blockIdx.y * low * high;
-  float acc[R][R] = {};
+  double sum[R][R] = {};
   const int c0 = (int)((long long)chunks * blockIdx.x / gridDim.x), c1 = (int)((long long)chunks * (blockIdx.x + 1) / gridDim.x);
   float v[kSmallChunk * L / kSmallThreads];
   fetch_chunk<T, TALL, L>(m, low, high, c0 * kSmallChunk, v, tid);
@@ -154,13 +157,18 @@ __global__ void __launch_bounds__(kSmallThreads) small_gram_kernel(const T* __re
     place_chunk<TALL, L>(v, low, high, c * kSmallChunk, f, xs, kPitch, 1, tid);
     __syncthreads();
     if (c + 1 < c1) fetch_chunk<T, TALL, L>(m, low, high, (c + 1) * kSmallChunk, v, tid);
+    float acc[R][R] = {};
     micro<R, R, kSmallChunk>(xs, kPitch, xs, kPitch, ty, tx, acc);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < R; ++j) sum[i][j] += (double)acc[i][j];
   }
   float* to = partial + ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * L * L;
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int j = 0; j < R; ++j) to[(R * ty + i) * L + R * tx + j] = acc[i][j];
+    for (int j = 0; j < R; ++j) to[(R * ty + i) * L + R * tx + j] = (float)sum[i][j];
 }
 
 // Q^T of each matrix from the parts of its Gram matrix, and the scale of X_0
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(kSmallThreads) small_iterate_kernel(const floa
   }
   const float* from = partial + (size_t)blockIdx.x * parts * L * L;
   constexpr int kQuads = kEach / 4;
-  float4 sum[kQuads] = {};
+  double sum[kQuads][4] = {};
 #pragma unroll 1
   for (int t = 0; t < parts; t += 4) {  // in the order of the parts; past the last: the last again, not added
     float4 v[4][kQuads];
@@ -194,12 +202,13 @@ __global__ void __launch_bounds__(kSmallThreads) small_iterate_kernel(const floa
       if (t + u < parts)
 #pragma unroll
         for (int i = 0; i < kQuads; ++i)
-          sum[i].x += v[u][i].x, sum[i].y += v[u][i].y, sum[i].z += v[u][i].z, sum[i].w += v[u][i].w;
+          sum[i][0] += v[u][i].x, sum[i][1] += v[u][i].y, sum[i][2] += v[u][i].z, sum[i][3] += v[u][i].w;
   }
 #pragma unroll
   for (int i = 0; i < kQuads; ++i) {
     const int e = 4 * (tid + i * kSmallThreads);
-    *reinterpret_cast<float4*>(A + e / L * kPitch + e % L) = sum[i];
+    *reinterpret_cast<float4*>(A + e / L * kPitch + e % L) =
+        make_float4((float)sum[i][0], (float)sum[i][1], (float)sum[i][2], (float)sum[i][3]);
   }
   __syncthreads();
   auto product = [&](const float* x, const float* y, float (&acc)[R][R]) {  // x^T y
