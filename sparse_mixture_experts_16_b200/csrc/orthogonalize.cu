@@ -43,20 +43,19 @@ constexpr int kPrepThreads = 256;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-template <typename T>
-__device__ __forceinline__ float load_value(const T* p);
-template <>
-__device__ __forceinline__ float load_value<float>(const float* p) { return __ldg(p); }
-template <>
-__device__ __forceinline__ float load_value<uint16_t>(const uint16_t* p) { return __uint_as_float((uint32_t)__ldg(p) << 16); }
+// What these kernels read, the caller's matrices too, the kernel before may write while they are resident already
+// (programmatic launch), and the short-side product runs in place.  All of it is therefore read by ordinary loads,
+// never as memory that nobody writes: no __ldg, no const __restrict__.
+__device__ __forceinline__ float load_value(const float* p) { return *p; }
+__device__ __forceinline__ float load_value(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 
 // eight values from p, which is 16-byte aligned
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
   const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -74,7 +73,7 @@ __device__ __forceinline__ void load8_tail(const T* p, int n, float (&v)[8]) {
 // partial[matrix][part] = sum of squares of the part's elements, in 64 bits and a fixed order.  Bound by
 // reading g once; `wide`: every matrix starts on 16 bytes.
 template <typename T>
-__global__ void __launch_bounds__(kPrepThreads) norm_kernel(const T* __restrict__ g, long long count, int wide,
+__global__ void __launch_bounds__(kPrepThreads) norm_kernel(const T* g, long long count, int wide,
                                                             double* __restrict__ partial) {
   __shared__ double warp_sum[kPrepThreads / 32];
   pdl_wait();
@@ -117,8 +116,8 @@ cudaError_t norms_of(const T* g, int count, int M, int N, double* norms, int& pa
 // hi + lo * 2^-11 = 2^12 g / ||g||, rows padded with zeros to the pitch; bound by reading g and writing
 // as many bytes.  `wide`: every row of g starts on 16 bytes.
 template <typename T>
-__global__ void __launch_bounds__(kPrepThreads) scale_kernel(const T* __restrict__ g, int M, int N, int ld, int wide,
-                                                             const double* __restrict__ partial, int parts,
+__global__ void __launch_bounds__(kPrepThreads) scale_kernel(const T* g, int M, int N, int ld, int wide,
+                                                             const double* partial, int parts,
                                                              uint16_t* __restrict__ hi, uint16_t* __restrict__ lo) {
   __shared__ double inv;
   pdl_wait();

@@ -87,7 +87,7 @@ __device__ __forceinline__ void micro(const float* x, int px, const float* y, in
 }
 
 // 1 / ||g|| from the norm's parts (0 for a zero matrix), 1 without parts; a whole warp
-__device__ __forceinline__ double small_scale(const double* __restrict__ norms, int parts, int lane) {
+__device__ __forceinline__ double small_scale(const double* norms, int parts, int lane) {
   if (parts == 0) return 1.0;
   double t = 0.0;
   for (int i = lane; i < parts; i += 32) t += norms[i];
@@ -132,8 +132,8 @@ __device__ __forceinline__ void place_chunk(const float (&v)[kSmallChunk * L / k
 
 // partial[matrix][part] = the part's share of X_0 X_0^T
 template <typename T, bool TALL, int L>
-__global__ void __launch_bounds__(kSmallThreads) small_gram_kernel(const T* __restrict__ g, int low, int high, int chunks,
-                                                                   const double* __restrict__ norms, int norm_parts,
+__global__ void __launch_bounds__(kSmallThreads) small_gram_kernel(const T* g, int low, int high, int chunks,
+                                                                   const double* norms, int norm_parts,
                                                                    float* __restrict__ partial) {
   constexpr int R = L / 16, kPitch = L + 4;
   __shared__ __align__(16) float xs[kSmallChunk * kPitch];
@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(kSmallThreads) small_gram_kernel(const T* __re
 
 // Q^T of each matrix from the parts of its Gram matrix, and the scale of X_0
 template <int L>
-__global__ void __launch_bounds__(kSmallThreads) small_iterate_kernel(const float* __restrict__ partial, int parts, int steps,
-                                                                      const double* __restrict__ norms, int norm_parts,
+__global__ void __launch_bounds__(kSmallThreads) small_iterate_kernel(const float* partial, int parts, int steps,
+                                                                      const double* norms, int norm_parts,
                                                                       float* __restrict__ q, float2* __restrict__ scales) {
   constexpr int R = L / 16, kPitch = L + 4, kEach = L * L / kSmallThreads;
   extern __shared__ __align__(16) float small_smem[];
@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(kSmallThreads) small_iterate_kernel(const floa
 // before any of it is written, by the same block
 template <typename T, bool TALL, int L, typename OUT>
 __global__ void __launch_bounds__(kSmallThreads) small_apply_kernel(const T* g, int low, int high, int chunks,
-                                                                    const float* __restrict__ q,
-                                                                    const float2* __restrict__ scales,
+                                                                    const float* q,
+                                                                    const float2* scales,
                                                                     OUT* out) {
   constexpr int R = L / 16, kPitch = L + 4, kXPitch = kSmallChunk + 4;
   __shared__ __align__(16) float qs[L * kPitch];
