@@ -387,7 +387,9 @@ moe_status_t moe_grouped_gemm_wgrad(const void* dy, const void* x, const int32_t
  * the matrix hardly has by up to a.  A matrix that holds a NaN or an infinity comes out as NaN; the others
  * of the batch are not affected.  Any sizes 1 <= M, N <= 65536, odd ones too; B >= 0; 1 <= steps <= 16 (5 is
  * usual).
- *   ws: as for moe_grouped_gemm; it holds a few matrices at a time, not the batch.
+ *   ws: as for moe_grouped_gemm; it holds the matrices that run side by side, not the batch: at most 90 MB where the
+ *       shorter side is at most 64, else at most 1.4 GB, or one matrix's 6 M N + 4 min(M, N)^2 bytes (of sides
+ *       rounded up to 16) and 40 MB if that is more.
  * ---------------------------------------------------------------------------------------- */
 size_t moe_orthogonalize_workspace_size(int B, int M, int N); /* 0 if a size is invalid */
 moe_status_t moe_orthogonalize(const void* g, int g_dtype, int B, int M, int N, int steps, moe_bf16_t* out, void* ws,

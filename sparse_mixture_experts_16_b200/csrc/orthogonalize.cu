@@ -302,7 +302,7 @@ extern "C" {
 size_t moe_orthogonalize_workspace_size(int B, int M, int N) {
   Layout l;
   if (!layout_of(B, M, N, l)) return 0;
-  return small_side(M, N) ? small_layout(B, M, N).total : l.total;
+  return small_side(M, N) ? small_workspace(B, M, N) : l.total;
 }
 
 moe_status_t moe_orthogonalize(const void* g, int g_dtype, int B, int M, int N, int steps, moe_bf16_t* out, void* ws,
@@ -321,7 +321,7 @@ moe_status_t moe_orthogonalize(const void* g, int g_dtype, int B, int M, int N, 
   uint8_t* b = static_cast<uint8_t*>(ws);
   cudaStream_t s = (cudaStream_t)stream;
   if (small_side(M, N)) {
-    const SmallLayout sl = small_layout(B, M, N);
+    const SmallLayout sl = small_layout(B, M, N, steps > kSmallSteps);
     for (int at = 0; at < B; at += sl.batch) {
       const int count = B - at < sl.batch ? B - at : sl.batch;
       const long long skip = (long long)at * M * N;

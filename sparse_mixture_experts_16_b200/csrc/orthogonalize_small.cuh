@@ -26,6 +26,7 @@ constexpr int kSmallSide = 64, kSmallSteps = 5;
 constexpr int kSmallThreads = 256;     // 16 x 16 threads, a micro tile each
 constexpr int kSmallChunk = 64;        // of the long side
 constexpr int kSmallBlocks = 592;      // 4 per SM: parts of the Gram matrices, slices of the products
+constexpr long long kSmallXBytes = 1LL << 26;  // of the fp32 X between rounds; one matrix has at most 2^24 bytes
 
 struct SmallLayout {
   int L, chunks, batch, parts;
@@ -34,14 +35,16 @@ struct SmallLayout {
 
 inline bool small_side(int M, int N) { return (M < N ? M : N) <= kSmallSide; }
 
-inline SmallLayout small_layout(int B, int M, int N) {
+// Matrices side by side and their places in the workspace.  `rounds`: more than kSmallSteps steps, with an X in
+// fp32 between them, and so few matrices at a time that X is bounded (and stays in L2).
+inline SmallLayout small_layout(int B, int M, int N, bool rounds) {
   SmallLayout l;
   const int low = M < N ? M : N, high = M < N ? N : M;
   l.L = low <= 32 ? 32 : 64;
   l.chunks = (high + kSmallChunk - 1) / kSmallChunk;
-  const long long fits = (1LL << 30) / (4LL * M * N);  // of the fp32 X between rounds
+  const long long fits = kSmallXBytes / (4LL * M * N);
   l.batch = B < kSmallBlocks ? B : kSmallBlocks;
-  if (l.batch > fits) l.batch = (int)fits;
+  if (rounds && l.batch > fits) l.batch = (int)fits;
   l.parts = kSmallBlocks / l.batch;
   if (l.parts > 32) l.parts = 32;  // one block adds them up
   if (l.parts > l.chunks) l.parts = l.chunks;
@@ -55,9 +58,15 @@ inline SmallLayout small_layout(int B, int M, int N) {
   l.scale = take((size_t)l.batch * sizeof(float2));
   l.partial = take((size_t)l.batch * l.parts * l.L * l.L * sizeof(float));
   l.q = take((size_t)l.batch * l.L * l.L * sizeof(float));
-  l.x = take((size_t)l.batch * M * N * sizeof(float));
+  l.x = take(rounds ? (size_t)l.batch * M * N * sizeof(float) : 0);
   l.total = at;
   return l;
+}
+
+// for any number of steps
+inline size_t small_workspace(int B, int M, int N) {
+  const size_t once = small_layout(B, M, N, false).total, rounds = small_layout(B, M, N, true).total;
+  return once > rounds ? once : rounds;
 }
 
 template <int R>
