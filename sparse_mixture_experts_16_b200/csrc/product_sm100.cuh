@@ -299,10 +299,11 @@ __device__ __forceinline__ int divide(int n, int d, float inv, int& rem) {
 // Rows of a tile of a group.  They are dealt evenly over its rt row tiles, in 16s: a tile of few rows costs
 // nearly half a full one, for the columns' operand comes in whole.  The symmetric products keep square tiles.
 template <int EPI>
-__device__ __forceinline__ int step_of(int rows, int rt, int lr) {
-  if (symmetric(EPI) || rt == 1) return 1 << lr;
+__host__ __device__ constexpr int step_of(int rows, int rt, int lr) {
+  if (symmetric(EPI) || rt <= 1) return 1 << lr;
   return ((rows + rt - 1) / rt + 15) / 16 * 16;
 }
+static_assert(step_of<kOut16>(0, 0, kMostLr) > 0, "no rows (every launch of ragged rows asks): no division by no tiles");
 
 // tab: kRaggedRows, kRaggedK: first row and rows of each group; kRaggedRows: then the first tile of each
 template <int RAGGED, int EPI>
