@@ -467,6 +467,8 @@ def moe_orthogonalize(g, steps=5, out=None, ws=None):
     M, N = g.shape[-2:]
     B = g.numel() // (M * N) if M * N else 0
     _need_int32("moe_orthogonalize", B, M, N)
+    if steps != int(steps) or not 1 <= steps <= 16:  # before ctypes drops upper bits
+        raise MoeError(1, "moe_orthogonalize")
     index = g.get_device()
     _need_at(g, g.dtype, g.shape, index, "g")
     if out is None:
