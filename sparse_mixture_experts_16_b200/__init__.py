@@ -348,18 +348,23 @@ def _product_ws(ws, need, index):
 
 def _on_stream(function):
     """Adds ``stream``: the call runs with it as the current stream, so that what the call allocates and
-    zeroes belongs to it too."""
+    zeroes belongs to it too; what it is given is not used again before ``stream`` has come past the call, even if
+    the caller lets go of it."""
     @functools.wraps(function)
     def call(*args, stream=None, **kwargs):
         if stream is None:
             return function(*args, **kwargs)
         import torch
 
-        device = next(a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor)).device
+        given = [a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor)]
+        device = given[0].device
         if device != stream.device:
             raise ValueError(f"stream: expected a stream on {device}, got {stream.device}")
         with torch.cuda.stream(stream):
-            return function(*args, **kwargs)
+            results = function(*args, **kwargs)
+        for t in given:
+            t.record_stream(stream)
+        return results
 
     return call
 
@@ -414,7 +419,8 @@ def moe_grouped_gemm(x, offsets, w, out=None, out_dtype=None, ws=None):
     """y[r] = x[r] @ w[e].T for the rows r of each expert segment e: x [M, K], w [E, N, K] (both bf16 or
     both fp16), offsets [E+1] int32 -> (y [M, N] in x's type or ``out_dtype`` = torch.float32, ws).
     Rows of ``out`` outside every segment are left as they were.  Pass the returned ws to later calls to keep
-    it, one call at a time.  ``stream``: run there; the operands have to be ready on it."""
+    it, one call at a time.  ``stream``: run there; the operands have to be ready on it, and may be let go of
+    after the call."""
     return _rows_product("moe_grouped_gemm", x, offsets, w, 2, 1, out, out_dtype, ws)
 
 
