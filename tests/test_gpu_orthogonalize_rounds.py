@@ -44,3 +44,54 @@ def test_short_sides_with_more_than_five_steps(cuda_device, shape, steps):
     assert moe.moe_get_device_error(ws) == 0
     assert (u[shape[0] // 2] == 0).all()
     assert off(u, iterate(g, steps)) < 2.0 ** -8 + 3.4e-3 * steps / 5
+
+
+TOL = 2.0 ** -8 + 3.4e-3
+
+
+@pytest.mark.parametrize("shape", [(1303, 65, 73), (700, 80, 65), (30, 96, 65536), (24, 65536, 90)], ids=str)
+def test_other_sides_in_several_rounds(cuda_device, shape):
+    """592 matrices at a time, dealt evenly (435, 435 and 433, where the second round's results start on an odd
+    element; 350 twice), or as many as 768 MB hold"""
+    b = shape[0]
+    g = gauss(*shape)
+    g[b // 2] = 0
+    u, ws = moe.moe_orthogonalize(g)
+    assert moe.moe_get_device_error(ws) == 0
+    assert (u[b // 2] == 0).all()
+    some = range(b) if b > 100 else (0, b // 2 - 1, b // 2 + 1, b - 1)
+    ref = iterate(g[list(some)])
+    assert off(u[list(some)], ref) < TOL
+    for i in (0, b - 1):
+        assert off(moe.moe_orthogonalize(g[i])[0][None], iterate(g[i:i + 1])) < TOL
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 65, 65536), (2, 65536, 66), (1, 130, 65521), (1, 65535, 257), (1, 4100, 4211)], ids=str)
+def test_long_sides(cuda_device, shape, dtype):
+    g = gauss(*shape).to(dtype)
+    u, ws = moe.moe_orthogonalize(g)
+    assert moe.moe_get_device_error(ws) == 0
+    assert off(u, iterate(g)) < TOL
+
+
+@pytest.mark.parametrize("shape", [(3, 70, 90), (3, 90, 70), (2, 129, 257), (2, 300, 136)], ids=str)
+def test_rows_behind_the_last_matrix_are_left_as_they_were(cuda_device, shape):
+    """the last step stores rows of any length, two bytes or sixteen at a time"""
+    b, m, n = shape
+    big = torch.full((b * m * n + 4096,), 7.0, dtype=torch.bfloat16, device="cuda")
+    g = gauss(*shape)
+    out = big[:b * m * n].view(shape)
+    moe.moe_orthogonalize(g, out=out)
+    assert (big[b * m * n:] == 7.0).all() and off(out, iterate(g)) < TOL
+
+
+def test_results_past_32_bits(cuda_device):
+    """2^31 elements and more: 515 matrices of [2048, 2048] in bf16, more than 4 GiB; the last and those around
+    2^31 elements are looked at"""
+    b, m, n = 515, 2048, 2048
+    g = torch.empty(b, m, n, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(4))
+    u, ws = moe.moe_orthogonalize(g)
+    assert moe.moe_get_device_error(ws) == 0
+    for i in (0, 511, 512, 514):
+        assert off(u[i:i + 1], iterate(g[i:i + 1])) < TOL
