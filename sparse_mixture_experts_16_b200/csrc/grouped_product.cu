@@ -114,7 +114,6 @@ moe_status_t moe_grouped_gemm_wgrad(const void* dy, const void* x, const int32_t
   p.rows = N;
   p.cols = K;
   p.kb_typ = (M / E + kBK - 1) / kBK;  // the mean segment
-  p.rows_typ = N;
   p.ld = K;
   const OperandHost out = {dw, (uint64_t)K, (uint64_t)N, (uint64_t)E};
   if (!set_output(p, out)) return MOE_ERR_CUDA;

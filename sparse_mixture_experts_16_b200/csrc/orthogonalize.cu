@@ -244,7 +244,6 @@ cudaError_t iterate(int count, int M, int N, int steps, const Layout& l, uint16_
     p.ld = l.lp;
     p.K = tall ? M : l.np;
     p.kb_typ = (p.K + kBK - 1) / kBK;
-    p.rows_typ = l.low;
     p.out = gram;
     p.c1 = kUnscale;
     if (tall) {
@@ -261,7 +260,6 @@ cudaError_t iterate(int count, int M, int N, int steps, const Layout& l, uint16_
     p.ld = l.lp;
     p.K = l.lp;
     p.kb_typ = (p.K + kBK - 1) / kBK;
-    p.rows_typ = l.low;
     p.out = poly;
     p.src = gram;
     p.c0 = kNsB;
@@ -273,7 +271,7 @@ cudaError_t iterate(int count, int M, int N, int steps, const Layout& l, uint16_
     p = base;
     p.K = l.lp;
     p.kb_typ = (p.K + kBK - 1) / kBK;
-    p.rows = p.rows_typ = p.ld = l.np;  // the product's rows and columns are exchanged
+    p.rows = p.ld = l.np;  // the product's rows and columns are exchanged
     p.cols = M;
     p.cols_out = N;
     p.src = hi[k & 1];

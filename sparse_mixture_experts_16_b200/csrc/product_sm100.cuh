@@ -132,7 +132,8 @@ struct alignas(64) Params {
   float* partial;
   int* counters;
   int prows;               // rows per partial tile
-  int kb_typ, rows_typ;    // K blocks and rows of a typical tile (the split's cost model)
+  int kb_typ;              // K blocks of a typical tile (the split's cost model)
+  int rows_typ;            // kRaggedRows: rows of the mean segment (the same)
   int withhold_first_load; // test only: the even CTA never issues its first stage's copies
   int* err;
 };
