@@ -29,11 +29,13 @@
 // the last part to arrive (an atomic counter per warp's share, no waiting) adds them in the order of
 // the parts, so results do not depend on timing.
 //
-// Rounding.  The tensor core truncates when it aligns an addend to its accumulator, which biases a
-// long sum towards zero: about 1e-9 of the sum for every k (measured on this GPU through a library
-// product with fp32 results: 1e-6 at k = 1024, 4.4e-6 at 4096, 1.9e-5 at 16384).  Where the result stays
-// fp32 (kPromote), the accumulator is therefore drained every 512 k into registers and added there,
-// rounded to nearest; a 16-bit result, 2^-9 wide, does not see it.
+// Rounding.  The tensor core truncates when it aligns an addend to its accumulator, which biases a long sum
+// towards zero.  Measured on this GPU through a library product with fp32 results, of the norm: terms of random
+// signs 1.0e-6 (bf16) and 1.3e-6 (fp16) at k = 1024, 4.4e-6 and 4.9e-6 at 4096, 1.9e-5 at 16384, about 1.1e-9 per
+// k; all-positive terms 2.2e-6 and 6.1e-6, 1.4e-5 and 2.6e-5, 8.3e-5 and 1.1e-4, about 5e-9 per k.  Where the
+// result stays fp32 (kPromote), the accumulator is therefore drained every 512 k into registers and added there,
+// rounded to nearest: 4.8e-7 and 6.5e-7, all-positive 9e-7 and 2.8e-6, at any k.  Of a 16-bit result, half a step of bf16 is
+// 3.9e-3 and of fp16 4.9e-4 of it: only all-positive terms of fp16 at k beyond 16384 come near that.
 //
 // Every wait is bounded (kWaitLimitNs); on expiry the kernel sets kErrTimeout and returns.
 #pragma once
