@@ -113,8 +113,8 @@ cudaError_t norms_of(const T* g, int count, int M, int N, double* norms, int& pa
 
 #include "orthogonalize_small.cuh"
 
-// hi + lo * 2^-11 = 2^12 g / ||g||, rows padded with zeros to the pitch; bound by reading g and writing
-// as many bytes.  `wide`: every row of g starts on 16 bytes.
+// hi + lo * 2^-11 = 2^12 g / ||g||, rows padded with zeros to the pitch, lo in low_index's order; bound by reading
+// g and writing as many bytes.  `wide`: every row of g starts on 16 bytes.
 template <typename T>
 __global__ void __launch_bounds__(kPrepThreads) scale_kernel(const T* g, int M, int N, int ld, int wide,
                                                              const double* partial, int parts,
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kPrepThreads) scale_kernel(const T* g, int M, 
       }
     }
     *reinterpret_cast<uint4*>(hi + base + 8LL * i) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4*>(lo + base + 8LL * i) = make_uint4(l[0], l[1], l[2], l[3]);
+    *reinterpret_cast<uint4*>(lo + low_index((int)blockIdx.y, (int)r, (int)c, M, ld)) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 
@@ -179,7 +179,7 @@ bool layout_of(int B, int M, int N, Layout& l) {
   l.np = (N + 15) / 16 * 16;
   const long long rt = (l.low + kTile - 1) / kTile, tiles = rt * (rt + 1) / 2;
   long long batch = (kTargetTiles + tiles - 1) / tiles;
-  const long long fits = kBatchBytes / (6LL * M * l.np);
+  const long long fits = kBatchBytes / (4LL * M * l.np + 2 * low_elements(1, M, l.np));
   if (batch > fits) batch = fits > 1 ? fits : 1;
   l.batch = B < batch ? B : (int)batch;
   l.prows = partial_rows(M > l.np ? M : l.np);
@@ -193,7 +193,7 @@ bool layout_of(int B, int M, int N, Layout& l) {
   l.norms = take((size_t)l.batch * kNormParts * sizeof(double));
   l.hi0 = take(x);
   l.hi1 = take(x);
-  l.lo = take(x);
+  l.lo = take((size_t)low_elements(l.batch, M, l.np) * 2);
   l.gram = take(s);
   l.poly = take(s);
   l.diag = take((size_t)l.batch * l.lp * sizeof(float));

@@ -122,10 +122,10 @@ struct alignas(64) Params {
   int rows, cols, K;       // rows (not kRaggedRows), columns and K (not kRaggedK) of a group
   uint32_t idesc;          // instruction descriptor without M and N
   int out_bf16;            // kOut16: bf16 instead of fp16
-  int ld;                  // row pitch of src, src_lo, out, out_lo of the Newton-Schulz epilogues
+  int ld;                  // row pitch of src and out of the Newton-Schulz epilogues (multiples of 16)
   int cols_out;            // kApply, kApplyLast: columns of a row of X that exist; the latter: row pitch of out
   void* out;
-  uint16_t* out_lo;        // kApply
+  uint16_t* out_lo;        // kApply: in low_index's order
   const uint16_t* src;     // kPoly: symmetric; kApply, kApplyLast: X's high-order part
   const uint16_t* src_lo;  // kApply, kApplyLast: its low-order part, may be out_lo
   float* diag;             // kPoly: written, kApply and kApplyLast: read; a group's stands at its number x diag_ld
@@ -409,11 +409,11 @@ __device__ __forceinline__ void store_sector(uint16_t* p, const uint32_t* w) {
                : "memory");
 }
 
-// Where the output's rows are the tile's columns (kApply by the choice of operands, the symmetric products by
-// symmetry) a lane's 32 values are 64 contiguous bytes of its own row, and nothing goes through shared
-// memory, which the operands of the MMAs keep busy: with chunks turned there kApply took 420 us on 8 matrices
-// of 2048 x 7168 and 49 on 6 of 2001 x 999, so 378 and 35.  Pitches are multiples of 16 elements, so whole sectors move, and so
-// are the rows of a tile or they end in zeros.
+// Where the output's rows are the tile's columns (kApply and kApplyLast by the choice of operands, the symmetric
+// products by symmetry) a lane's 32 values are 64 contiguous bytes of its own row, and nothing goes through shared
+// memory, which the operands of the MMAs keep busy (with chunks turned there, and the low-order part alone added,
+// kApply took 420 us on 8 matrices of 2048 x 7168 and 49 on 6 of 2001 x 999, so 378 and 35).  Pitches are multiples of 16
+// elements, so whole sectors move, and so are the rows of a tile or they end in zeros.
 __device__ __forceinline__ long long lane_row(const Params& p, const Item& x, int rows, int j0, int col) {
   return ((long long)x.g * rows + col) * p.ld + x.r0 + j0;
 }
@@ -421,6 +421,15 @@ __device__ __forceinline__ void store_lane_row(uint16_t* o, const uint32_t (&w)[
   store_sector(o, w);
   if (nj > 16) store_sector(o + 16, w + 8);
 }
+
+// X's low-order part is no operand of a product, so it lies as the epilogues take it: blocks of 32 rows x 16
+// columns, one row's 16 (a lane's sector) after the other, and a warp's load or store is 1 KB in one piece.  In rows, as
+// hi, each touches 32 lines, and their number is what bounds these epilogues: 6 x [2001, 999] took 425 us so and takes
+// 380, 8 x [1024, 4096] 1038 and 950, 8 x [2048, 7168] 3590 and 3405.  Index of an element of matrix g:
+__device__ __forceinline__ long long low_index(int g, int row, int column, int rows, int ld) {
+  return (((long long)g * ((rows + 31) / 32) + row / 32) * (ld / 16) + column / 16) * 512 + row % 32 * 16 + column % 16;
+}
+inline long long low_elements(int groups, int rows, int ld) { return (long long)groups * ((rows + 31) / 32 * 32) * ld; }
 
 // what kPoly, kApply and kApplyLast add to a chunk: read one chunk ahead
 template <int EPI>
@@ -439,8 +448,9 @@ __device__ __forceinline__ void load_addend(const Params& p, const Item& x, Adde
     load_sector(p.src + at, s.hi);
     if (two) load_sector(p.src + at + 16, s.hi + 8);
     if constexpr (applies(EPI)) {
-      load_sector(p.src_lo + at, s.lo);
-      if (two) load_sector(p.src_lo + at + 16, s.lo + 8);
+      const uint16_t* lo = p.src_lo + low_index(x.g, col, x.r0 + j0, rows, p.ld);
+      load_sector(lo, s.lo);
+      if (two) load_sector(lo + 512, s.lo + 8);
     }
   }
   if constexpr (applies(EPI)) {
@@ -479,7 +489,8 @@ __device__ __forceinline__ void store_turned(uint16_t* o, int pitch, uint8_t* bu
 
 // A warp's chunk of kApplyLast, w[i] = elements j0 + 2 i and + 1 of row col of X (this lane's), turned through
 // shared memory (16 bytes at a time, permuted within a row so that no two lanes meet in a bank) so that a
-// row's 64 bytes lie side by side in a store.  Of another pitch than whole 16 bytes, a row at a time.
+// row's 64 bytes lie side by side in a store: 417 -> 376 us of this launch for 8 x [2048, 7168], against 16 bytes of
+// each lane's own row.  Of another pitch than whole 16 bytes, an element a lane, a row at a time.
 __device__ __forceinline__ void store_rows(const Params& p, const Item& x, uint8_t* buf, const uint32_t (&w)[16], int j0,
                                            int nj, int col, int lane) {
   const int pitch = p.cols_out, c0 = x.r0 + j0;
@@ -546,9 +557,10 @@ __device__ __forceinline__ void emit(const Params& p, const Item& x, uint8_t* bu
     if constexpr (EPI == kApplyLast) {
       store_rows(p, x, buf, hi, j0, nj, col, lane);
     } else if (col < p.cols) {
-      const long long at = lane_row(p, x, p.cols, j0, col);
-      store_lane_row(out + at, hi, nj);
-      store_lane_row(p.out_lo + at, lo, nj);
+      store_lane_row(out + lane_row(p, x, p.cols, j0, col), hi, nj);
+      uint16_t* o = p.out_lo + low_index(x.g, col, x.r0 + j0, p.cols, p.ld);
+      store_sector(o, lo);
+      if (nj > 16) store_sector(o + 512, lo + 8);
     }
   } else {
     uint32_t w[16];
@@ -677,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   cluster_sync();  // both CTAs' barriers and tensor memory are ready before either is used remotely
   tc_fence_after();
   // Segments are read from memory that the kernel before may have written; the schedule of equal groups is
-  // not, so there the producer and the epilogue wait before their own first access: 118 -> 111 us for
+  // not, so there the producer and the epilogue wait before their own first access: 136 -> 128 us for
   // 16 x [512, 256].
   if constexpr (RAGGED != kDense) pdl_wait();
   pdl_trigger();
