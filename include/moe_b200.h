@@ -389,7 +389,7 @@ moe_status_t moe_grouped_gemm_wgrad(const void* dy, const void* x, const int32_t
  * usual).
  *   ws: as for moe_grouped_gemm; it holds the matrices that run side by side, not the batch: at most 90 MB where the
  *       shorter side is at most 64, else at most 1.4 GB, or one matrix's 6 M N + 4 min(M, N)^2 bytes (of sides
- *       rounded up to 16) and 40 MB if that is more.
+ *       rounded up to 16) and 45 MB if that is more.
  * ---------------------------------------------------------------------------------------- */
 size_t moe_orthogonalize_workspace_size(int B, int M, int N); /* 0 if a size is invalid */
 moe_status_t moe_orthogonalize(const void* g, int g_dtype, int B, int M, int N, int steps, moe_bf16_t* out, void* ws,

@@ -167,8 +167,8 @@ struct Layout {
 };
 
 // Enough matrices side by side that the launch with the fewest tiles, the Gram matrix's, fills eight rounds
-// of 74 clusters, within 768 MB of X.  With one round's worth 300 x [128, 128] took 510 us, with four 304, now
-// 216; 8 x [2048, 7168] 4062, 3451 and 3493.
+// of 74 clusters, within 768 MB of X.  With one round's worth 300 x [128, 128] took 546 us, with four 323, with
+// eight 237; 8 x [2048, 7168] 4225, 3670 and 3680 (one build, before the low-order part's present order).
 constexpr long long kTargetTiles = 592;
 constexpr long long kBatchBytes = 3LL << 28;
 

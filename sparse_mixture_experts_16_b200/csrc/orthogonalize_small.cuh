@@ -1,7 +1,8 @@
 // orthogonalize_small.cuh -- the Newton-Schulz iterate of matrices whose shorter side is at most 64
 // (router weights, low-rank factors, heads).  The products of the general path would fill a corner of a
-// tile each, and its launches, three per step, cost 65 to 220 us whatever the work: 13 x [202, 29] took 68 us
-// there and 18 here, 9 x [32, 6645] 190 and 44, 64 x [7168, 64] 555 and 382, and 60 x [2000, 40] 181 and 186.
+// tile each, and its launches, three per step, cost 65 to 340 us whatever the work.  Both paths measured, there and
+// here, us: 13 x [202, 29] 73 and 19, 1 x [64, 64] 65 and 48, 9 x [32, 6645] 226 and 48, 300 x [64, 64] 156 and 125,
+// 60 x [2000, 40] 197 and 153, 700 x [40, 56] 325 and 242, 64 x [7168, 64] 643 and 347, 512 x [16, 7168] 5400 and 880.
 // Every iterate is a polynomial of A_0 = X_0 X_0^T times X_0, so the iteration runs on [L, L] matrices alone
 // (L = 32 or 64):
 //     Q = I, A = A_0;  P = a I + b A + c A A;  Q <- P Q;  A <- P A P;  ...;  X = Q X_0
